@@ -314,6 +314,163 @@ int rrq_attention_decode_noalloc(const void* q, int hq, const uint8_t* k_codes,
 size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_bits, int64_t T);
 
 /*
+ * rrq_attention_shared — one decode step of attention for a batch of sequences
+ * that share a quantised prefix, each followed by a quantised tail of its own.
+ * The pages define the quantised cache ("Attn-rot (TurboQuant lite) in llama.cpp"
+ * page, "What kind of beast is Attn-rot": K and V both quantised after a rotation;
+ * "Random-rotation quantization" page, "Three decoders, one rotation": the MSE
+ * decoder); serving a batch from it is this library's addition.  For sequence b and
+ * query head h, g = ⌊h·hkv/hq⌋, over the tokens t of the prefix and then of the
+ * first n_b = tail_lens[b] rows of tail b:
+ *     s[t] = scale · <q_{b,h}, k̂_{t,g}>,   p = softmax(s),   out_{b,h} = Σ_t p[t]·v̂_{t,g},
+ * k̂ and v̂ as rrq_decode.  The prefix is read and dequantised once for the whole
+ * batch.  A sequence without any token (no prefix and n_b = 0) gets zeros.
+ *   q           [batch × hq × d] of q_dtype (RRQ_F16 or RRQ_BF16), unrotated
+ *   pk_codes    [prefix·hkv × d·k_bits/8] bytes, row t·hkv + g;  pk_norms [prefix·hkv]
+ *   pv_codes    [prefix·hkv × d·v_bits/8] bytes;                 pv_norms [prefix·hkv]
+ *   tk_codes    [batch·tail_cap·hkv × d·k_bits/8] bytes, row (b·tail_cap + t)·hkv + g;
+ *   tk_norms, tv_codes, tv_norms likewise
+ *   tail_lens   [batch] int32 on the device, read by the kernels: values outside
+ *               [0, tail_cap] count as the nearer end.  Rows behind n_b are not read.
+ *   workspace   device scratch of workspace_bytes ≥ rrq_attention_shared_workspace_bytes(
+ *               batch, hq, hkv, d, prefix, tail_cap), 256-byte aligned, of any content.
+ *               Calls that share a workspace must not overlap on the GPU (also where
+ *               they were captured into graphs).
+ *   out         [batch × hq × d] of q_dtype (output)
+ * prefix ≥ 0 and tail_cap ≥ 0; the arrays of a part of size 0 (and tail_lens with
+ * tail_cap = 0) may be NULL.  batch = 0 is a no-op.  d ∈ {64, 128, 256, 512}, 1- to
+ * 4-bit K and V; hq a multiple of hkv, at most 128 query heads per kv head.
+ * Alignment: codes, q and out 16 bytes, norms and tail_lens 4.
+ * Accuracy: softmax statistics, sums and the rotations in fp32.  For d ≤ 256 both
+ * products run on the tensor cores with fp16 operands and fp32 sums; value weights
+ * are scaled so that value norms within 2^-20 of the largest one keep their precision.
+ * Per head the output is within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is
+ * rounded to q_dtype.
+ * Errors: RRQ_ERR_INVALID (incl. a workspace that is too small), RRQ_ERR_UNSUPPORTED
+ * (q_dtype RRQ_F32, more than 128 heads per kv head, 2^30 or more 64-token tiles, or a
+ * device whose per-block reserved shared memory is not the 1 KB that the tensor-core
+ * kernel's layout assumes), RRQ_ERR_CUDA.
+ */
+int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,
+                         const uint8_t* pk_codes, const float* pk_norms, const uint8_t* pv_codes,
+                         const float* pv_norms, int64_t prefix, const uint8_t* tk_codes,
+                         const float* tk_norms, const uint8_t* tv_codes, const float* tv_norms,
+                         int64_t tail_cap, const int32_t* tail_lens, int hkv, int d, int k_bits,
+                         uint64_t k_seed, const float* k_codebook, int v_bits, uint64_t v_seed,
+                         const float* v_codebook, float scale, void* workspace,
+                         size_t workspace_bytes, void* out, void* stream);
+
+/*
+ * rrq_attention_shared_workspace_bytes — the workspace rrq_attention_shared needs
+ * on the current device (it depends on the SM count), or 0 for an invalid or
+ * unsupported shape.  It grows with batch, hq and d, and with prefix and tail_cap
+ * only until every SM has work.
+ */
+size_t rrq_attention_shared_workspace_bytes(int64_t batch, int hq, int hkv, int d, int64_t prefix,
+                                            int64_t tail_cap);
+
+/*
+ * rrq_attention_mass — the attention weight that every cached token has drawn so
+ * far, from a decode step's scores (rrq_qk_scores, rrq_qk_scores_qjl): what
+ * rrq_evict keeps tokens by.  Not on the pages.  With p = softmax of a head's
+ * scores over the tokens t < n_b = lens[b]:
+ *     out[b][g][t] = decay · mass[b][g][t] + Σ_{h in group g} p[b][h][t],   t < n_b,
+ *     out[b][g][t] = mass[b][g][t],                                        t ≥ n_b.
+ * A score of −inf masks its token (weight 0); a head whose scores are all −inf adds
+ * nothing.  +inf and NaN scores give unspecified values for the tokens of their
+ * kv head (no fault).
+ *   scores  [batch × hq × T] float
+ *   lens    [batch] int32 on the device, or NULL (all T tokens); values outside
+ *           [0, T] count as the nearer end
+ *   mass    [batch × hkv × T] float, or NULL (zeros);  out may be the same array
+ *   out     [batch × hkv × T] float (output)
+ * hq a multiple of hkv.  batch = 0 or T = 0 is a no-op.  T < 2^31.  Arrays 4-byte
+ * aligned (16-byte vectors are used where addresses and T allow).  fp32 throughout;
+ * the result does not depend on the order in which the GPU runs blocks.
+ * Errors: RRQ_ERR_INVALID (incl. a decay that is not finite), RRQ_ERR_CUDA.
+ */
+int rrq_attention_mass(const float* scores, int64_t batch, int hq, int hkv, int64_t T,
+                       const int32_t* lens, float decay, const float* mass, float* out,
+                       void* stream);
+
+/*
+ * rrq_evict — cut every sequence of a quantised cache back to at most `keep` tokens
+ * per kv head: the first `sink` tokens and the last `recent` ones stay, the others
+ * by the largest mass (rrq_attention_mass), equal masses in favour of the lower
+ * token.  Not on the pages.  The kept rows move, in their order, to the front of
+ * another cache; each kv head keeps tokens of its own.  With n_b = lens[b]:
+ *     m_b = min(n_b, keep) → out_lens[b];
+ *     index[b][g][s] = the s-th kept token (ascending), s < m_b;
+ *     row (b·keep + s)·hkv + g of the output cache = row (b·cap + index[b][g][s])·hkv + g;
+ *     out_mass[b][g][s] = mass[b][g][index[b][g][s]].
+ * Entries s ≥ m_b of every output are left as they were.
+ *   mass      [batch × hkv × cap] float (a NaN counts as less than −inf, −0 as +0)
+ *   lens      [batch] int32 on the device, or NULL (all cap tokens); values outside
+ *             [0, cap] count as the nearer end
+ *   k_codes   [batch·cap·hkv × d·k_bits/8] bytes;  k_norms [batch·cap·hkv] float;
+ *   v_codes, v_norms likewise
+ *   index     [batch × hkv × keep] int32;  out_lens [batch] int32;
+ *   out_mass  [batch × hkv × keep] float, or NULL;
+ *   ok_codes, ok_norms, ov_codes, ov_norms: the output cache of capacity keep
+ * Inputs and outputs must not overlap.  keep ≥ 1, sink, recent ≥ 0 with
+ * sink + recent ≤ keep; cap < 2^31.  batch = 0 or cap = 0: out_lens is set to 0 for
+ * every sequence, nothing else is written.  Alignment: codes 16 bytes, the rest 4.
+ * Errors: RRQ_ERR_INVALID, RRQ_ERR_CUDA.
+ */
+int rrq_evict(const float* mass, int64_t batch, int hkv, int64_t cap, const int32_t* lens,
+              int64_t keep, int64_t sink, int64_t recent, int d, int k_bits, int v_bits,
+              const uint8_t* k_codes, const float* k_norms, const uint8_t* v_codes,
+              const float* v_norms, int32_t* index, int32_t* out_lens, float* out_mass,
+              uint8_t* ok_codes, float* ok_norms, uint8_t* ov_codes, float* ov_norms, void* stream);
+
+/* frequency schedules of rrq_rope_frequencies */
+#define RRQ_ROPE_NONE 0
+#define RRQ_ROPE_LINEAR 1
+#define RRQ_ROPE_NTK 2
+#define RRQ_ROPE_YARN 3
+
+/*
+ * rrq_rope_frequencies — rotary frequencies for rrq_rope, on the HOST, in double.
+ * Not on the pages.  For the pair i < rot/2 the unscaled frequency is
+ * θ_i = base^(−2i/rot) radians per position, and with the stretch f ≥ 1:
+ *   RRQ_ROPE_NONE    θ_i
+ *   RRQ_ROPE_LINEAR  θ_i / f (positions interpolated)
+ *   RRQ_ROPE_NTK     (base·f^(rot/(rot−2)))^(−2i/rot) (θ_i for rot = 2)
+ *   RRQ_ROPE_YARN    θ_i·(1 − r_i) + θ_i/f·r_i, where r_i rises linearly from 0 at the
+ *                    pair that turns `fast` times over `original` positions to 1 at
+ *                    the pair that turns `slow` times: r_i = clamp((i − lo)/(hi − lo), 0, 1),
+ *                    lo = max(⌊c(fast)⌋, 0), hi = min(⌈c(slow)⌉, rot − 1), hi − lo at least
+ *                    0.001, c(n) = rot·ln(original/(2πn))/(2 ln base)
+ * *factor is the factor on cos and sin: 0.1·ln f + 1 for YARN, else 1.
+ *   freqs   HOST, double[rot/2] (output);  factor HOST, double (output)
+ * rot even in [2, 512]; base > 1 and stretch ≥ 1 finite; for YARN original > 0 and
+ * fast ≥ slow > 0, finite.  Errors: RRQ_ERR_INVALID.  Thread-safe; no CUDA call.
+ */
+int rrq_rope_frequencies(int schedule, int rot, double base, double stretch, double original,
+                         double fast, double slow, double* freqs, double* factor);
+
+/*
+ * rrq_rope — rotary positions of queries and keys, before rrq_encode and the scores.
+ * Not on the pages.  Vector x of a token at position p: for the pair i < rot/2,
+ * (a, b) = (x_i, x_{i + rot/2}) (interleaved = 0) or (x_{2i}, x_{2i+1}) (interleaved = 1),
+ *     (a', b') = factor · (a·cos φ − b·sin φ, a·sin φ + b·cos φ),   φ = p·freqs[i],
+ * and coordinates from rot on are copied.  inverse = 1 takes −φ: the transposed map,
+ * which is also the gradient with respect to x.
+ * The angle is formed as p times the frequency in turns as a 64-bit fixed-point
+ * fraction, modulo one turn: within |p|·2^-65 turns of the exact one.  Products in
+ * fp32, rounded once to dtype.
+ *   x          [n × heads × d] of dtype;  y the same (output), which may be x itself
+ *   positions  [n] int64 on the device, of any sign
+ *   freqs      HOST, double[rot/2], finite, |freqs| < 2^31
+ * d ∈ {64, 128, 256, 512}; rot even in [2, d]; heads ≥ 1; n = 0 is a no-op.  Alignment:
+ * x and y 16 bytes, positions 8.
+ * Errors: RRQ_ERR_INVALID (incl. a factor that is not finite), RRQ_ERR_CUDA.
+ */
+int rrq_rope(const void* x, int dtype, int64_t n, int heads, int d, int rot, int interleaved,
+             const int64_t* positions, const double* freqs, double factor, int inverse, void* y,
+             void* stream);
+
+/*
  * rrq_q4_0_rot — "Attn-rot" (TurboQuant lite): rotate, then q4_0.
  * "Attn-rot (TurboQuant lite) in llama.cpp" page: rotate K/V before an
  * ordinary block format, q4_0 first of all.  With y = Πx (rotate = 1) or

@@ -31,7 +31,10 @@ Module map:
 * ``sphere``    — the sphere marginal (Beta density) and the DRIVE scales, used
                   only to pin the rotation against the page's statements.
 
+* ``serving``   — shared-prefix attention, accumulated attention weights, eviction and
+                  rotary positions (not on the pages).
+
 Parity status of each function is stated in its module header.
 """
 
-from . import rng, hadamard, codebook, rrq, q4_0, qjl, sphere  # noqa: F401
+from . import rng, hadamard, codebook, rrq, q4_0, qjl, sphere, serving  # noqa: F401

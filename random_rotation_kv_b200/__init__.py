@@ -17,11 +17,15 @@ from .binding import (  # noqa: F401
     RRQError,
     lib,
     rrq_attention_decode,
+    rrq_attention_mass,
+    rrq_attention_shared,
+    rrq_attention_shared_workspace_bytes,
     rrq_attention_workspace_bytes,
     rrq_codebook,
     rrq_decode,
     rrq_drive_encode,
     rrq_encode,
+    rrq_evict,
     rrq_format_version,
     rrq_ggml_block_bytes,
     rrq_ggml_rot,
@@ -31,6 +35,8 @@ from .binding import (  # noqa: F401
     rrq_qjl_matrix,
     rrq_qk_scores,
     rrq_qk_scores_qjl,
+    rrq_rope,
+    rrq_rope_frequencies,
     rrq_rotate,
     strerror,
 )

@@ -21,12 +21,14 @@ RRQ_OK, RRQ_ERR_INVALID, RRQ_ERR_CUDA, RRQ_ERR_UNSUPPORTED, RRQ_ERR_SCRATCH = 0,
 RRQ_F32, RRQ_F16, RRQ_BF16 = 0, 1, 2
 DTYPE_CODE = {torch.float32: RRQ_F32, torch.float16: RRQ_F16, torch.bfloat16: RRQ_BF16}
 # GGML block types (ggml's own type numbers), as in include/rrq.h
+ROPE_SCHEDULES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 GGML_TYPES = {"q4_0": 2, "q4_1": 3, "q5_0": 6, "q5_1": 7, "q8_0": 8}
 
 _c_i64 = ctypes.c_int64
 _c_u64 = ctypes.c_uint64
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
+_dbl = ctypes.c_double
 _fp = ctypes.POINTER(ctypes.c_float)
 
 # name -> (restype, argtypes), mirroring include/rrq.h
@@ -55,6 +57,15 @@ SIGNATURES = {
     "rrq_ggml_rot": (_int, [_vp, _int, _c_i64, _int, _c_u64, _int, _int, _vp, _vp]),
     "rrq_ggml_rot_decode": (_int, [_vp, _int, _c_i64, _int, _c_u64, _int, _vp, _int, _vp]),
     "rrq_qjl_matrix": (_int, [_c_u64, _int, _vp]),
+    "rrq_attention_shared": (_int, [_vp, _int, _c_i64, _int, _vp, _vp, _vp, _vp, _c_i64, _vp, _vp, _vp,
+                                    _vp, _c_i64, _vp, _int, _int, _int, _c_u64, _vp, _int, _c_u64, _vp,
+                                    ctypes.c_float, _vp, ctypes.c_size_t, _vp, _vp]),
+    "rrq_attention_shared_workspace_bytes": (ctypes.c_size_t, [_c_i64, _int, _int, _int, _c_i64, _c_i64]),
+    "rrq_attention_mass": (_int, [_vp, _c_i64, _int, _int, _c_i64, _vp, ctypes.c_float, _vp, _vp, _vp]),
+    "rrq_evict": (_int, [_vp, _c_i64, _int, _c_i64, _vp, _c_i64, _c_i64, _c_i64, _int, _int, _int, _vp, _vp,
+                         _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "rrq_rope_frequencies": (_int, [_int, _int, _dbl, _dbl, _dbl, _dbl, _dbl, _vp, _vp]),
+    "rrq_rope": (_int, [_vp, _int, _c_i64, _int, _int, _int, _int, _vp, _vp, _dbl, _int, _vp, _vp]),
 }
 
 
@@ -408,3 +419,218 @@ def rrq_qjl_matrix(seed: int, d: int, device=None) -> torch.Tensor:
     _check(lib().rrq_qjl_matrix(seed, d, _vp(host.ctypes.data)), "rrq_qjl_matrix")
     t = torch.from_numpy(host.view(np.int16).copy()).view(torch.bfloat16).reshape(d, d)
     return t if device is None else t.to(device)
+
+
+def _on_device(first: torch.Tensor, *others) -> torch.cuda.device:
+    """Context in which `first`'s device is the current one (a no-op where it is already);
+    the other tensors must live there too."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and on {t.device}")
+    return torch.cuda.device(first.device)
+
+
+def _cache_part(codes, norms, lead, hkv, row, what):
+    """Checks one K or V array pair of `lead` × hkv rows of `row` bytes."""
+    _dev_tensor(codes, f"{what}_codes", (torch.uint8,))
+    _dev_tensor(norms, f"{what}_norms", (torch.float32,))
+    if norms.numel() != lead * hkv or codes.numel() != lead * hkv * row:
+        raise ValueError(f"{what}_codes / {what}_norms have the wrong size")
+
+
+def rrq_attention_shared(q: torch.Tensor, pk_codes, pk_norms, pv_codes, pv_norms, tk_codes, tk_norms,
+                         tv_codes, tv_norms, tail_lens, hkv: int, d: int, k_seed: int, v_seed: int,
+                         k_bits: int = 4, v_bits: int = 4, k_codebook=None, v_codebook=None,
+                         scale: float = 1.0, out=None, workspace=None):
+    """One decode step of attention for a batch: out [batch, hq, d] of q's dtype (fp16 or
+    bf16) for unrotated queries q [batch, hq, d] over a shared quantised prefix
+    (pk_*, pv_*: rows t*hkv + g, or None without a prefix) followed by the first
+    tail_lens[b] rows of each sequence's own tail (tk_*, tv_*: [batch, cap, hkv, ...],
+    or None without tails; tail_lens int32 [batch] on the device).  A sequence without
+    any token gets zeros.
+
+    ``workspace``: a uint8 device tensor of at least
+    rrq_attention_shared_workspace_bytes(...) bytes, of any content; allocated when none
+    is given."""
+    _dev_tensor(q, "q", (torch.float16, torch.bfloat16))
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [batch, hq, d]")
+    if hkv < 1:
+        raise ValueError("hkv must be at least 1")
+    batch, hq = q.shape[:2]
+    prefix = cap = 0
+    if pk_codes is not None:
+        _dev_tensor(pk_norms, "pk_norms", (torch.float32,))
+        prefix = pk_norms.numel() // hkv
+        _cache_part(pk_codes, pk_norms, prefix, hkv, d * k_bits // 8, "pk")
+        _cache_part(pv_codes, pv_norms, prefix, hkv, d * v_bits // 8, "pv")
+    if tk_codes is not None:
+        _dev_tensor(tk_norms, "tk_norms", (torch.float32,))
+        cap = tk_norms.numel() // (batch * hkv) if batch else 0
+        _cache_part(tk_codes, tk_norms, batch * cap, hkv, d * k_bits // 8, "tk")
+        _cache_part(tv_codes, tv_norms, batch * cap, hkv, d * v_bits // 8, "tv")
+        _dev_tensor(tail_lens, "tail_lens", (torch.int32,))
+        if tail_lens.numel() != batch:
+            raise ValueError("tail_lens must hold one length per sequence")
+    if out is None:
+        out = torch.empty_like(q)
+    _dev_tensor(out, "out", (q.dtype,))
+    if out.numel() != q.numel():
+        raise ValueError("out has the wrong size")
+    with _on_device(q, pk_codes, pk_norms, pv_codes, pv_norms, tk_codes, tk_norms, tv_codes, tv_norms,
+                    tail_lens, out, workspace):
+        if workspace is None:
+            workspace = torch.empty(rrq_attention_shared_workspace_bytes(batch, hq, hkv, d, prefix, cap),
+                                    dtype=torch.uint8, device=q.device)
+        _dev_tensor(workspace, "workspace", (torch.uint8,))
+        kc, vc = _HostFloats(k_codebook), _HostFloats(v_codebook)
+        _check(lib().rrq_attention_shared(
+            _ptr(q), DTYPE_CODE[q.dtype], batch, hq, _ptr(pk_codes), _ptr(pk_norms), _ptr(pv_codes),
+            _ptr(pv_norms), prefix, _ptr(tk_codes), _ptr(tk_norms), _ptr(tv_codes), _ptr(tv_norms), cap,
+            _ptr(tail_lens), hkv, d, k_bits, k_seed, kc.ptr, v_bits, v_seed, vc.ptr, float(scale),
+            _ptr(workspace), workspace.numel(), _ptr(out), _stream(q)), "rrq_attention_shared")
+    return out
+
+
+def rrq_attention_shared_workspace_bytes(batch: int, hq: int, hkv: int, d: int, prefix: int,
+                                         tail_cap: int) -> int:
+    """Workspace bytes rrq_attention_shared needs on the current device."""
+    return int(lib().rrq_attention_shared_workspace_bytes(batch, hq, hkv, d, prefix, tail_cap))
+
+
+def rrq_attention_mass(scores: torch.Tensor, hkv: int, mass=None, lens=None, decay: float = 1.0, out=None):
+    """Softmax weights of scores [batch, hq, T] (or [hq, T], as rrq_qk_scores returns them)
+    summed over the query heads of each kv head and added to decay * mass: float32
+    [batch, hkv, T] (or [hkv, T]).
+
+    ``lens``: int32 [batch] on the device; tokens behind a sequence's length keep their
+    mass.  ``mass``: the sums so far, zeros when not given.  ``out`` may be ``mass``."""
+    _dev_tensor(scores, "scores", (torch.float32,))
+    if scores.dim() not in (2, 3):
+        raise ValueError("scores must be [batch, hq, T] or [hq, T]")
+    batch = scores.shape[0] if scores.dim() == 3 else 1
+    hq, t_len = scores.shape[-2:]
+    if hkv < 1:
+        raise ValueError("hkv must be at least 1")
+    if out is None:
+        out = torch.empty(*scores.shape[:-2], hkv, t_len, dtype=torch.float32, device=scores.device)
+    _dev_tensor(out, "out", (torch.float32,))
+    if out.numel() != batch * hkv * t_len:
+        raise ValueError("out has the wrong size")
+    if mass is not None:
+        _dev_tensor(mass, "mass", (torch.float32,))
+        if mass.numel() != batch * hkv * t_len:
+            raise ValueError("mass has the wrong size")
+    if lens is not None:
+        _dev_tensor(lens, "lens", (torch.int32,))
+        if lens.numel() != batch:
+            raise ValueError("lens must hold one length per sequence")
+    with _on_device(scores, mass, lens, out):
+        _check(lib().rrq_attention_mass(_ptr(scores), batch, hq, hkv, t_len, _ptr(lens), float(decay),
+                                        _ptr(mass), _ptr(out), _stream(scores)), "rrq_attention_mass")
+    return out
+
+
+def rrq_evict(mass: torch.Tensor, lens, keep: int, k_codes: torch.Tensor, k_norms: torch.Tensor,
+              v_codes: torch.Tensor, v_norms: torch.Tensor, sink: int = 0, recent: int = 0, index=None,
+              out_lens=None, out_mass=None, out=None):
+    """Cut a quantised cache back to `keep` tokens per kv head: the first `sink`, the last
+    `recent`, and the largest mass [batch, hkv, cap] (ties to the lower token).
+
+    k_codes [batch, cap, hkv, d*k_bits/8], k_norms [batch, cap, hkv], v_* alike; lens int32
+    [batch] on the device or None.  Returns (index int32 [batch, hkv, keep], out_lens int32
+    [batch], out_mass [batch, hkv, keep], k_codes, k_norms, v_codes, v_norms of capacity
+    `keep`).  ``out``: the four arrays of the new cache; entries behind a sequence's new
+    length are left as they were (zeros, and -1 in index, where this call allocates)."""
+    _dev_tensor(mass, "mass", (torch.float32,))
+    if mass.dim() != 3:
+        raise ValueError("mass must be [batch, hkv, cap]")
+    batch, hkv, cap = mass.shape
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    dev = mass.device
+    for t_, nm in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+        _dev_tensor(t_, nm, (torch.uint8,))
+        if t_.dim() != 4 or t_.shape[:3] != (batch, cap, hkv):
+            raise ValueError(f"{nm} must be [batch, cap, hkv, row bytes]")
+    for t_, nm in ((k_norms, "k_norms"), (v_norms, "v_norms")):
+        _dev_tensor(t_, nm, (torch.float32,))
+        if t_.shape != (batch, cap, hkv):
+            raise ValueError(f"{nm} must be [batch, cap, hkv]")
+    # a row of 8·w bytes is d = 64·w codes of one bit, or any other d and width of that product
+    widths = []
+    for t_, nm in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+        row = t_.shape[3]
+        shapes = [(dd, row * 8 // dd) for dd in (64, 128, 256, 512) if row * 8 % dd == 0 and 1 <= row * 8 // dd <= 4]
+        if not shapes:
+            raise ValueError(f"{nm}: no d and bit width give rows of {row} bytes")
+        widths.append(dict(shapes))
+    common = [dd for dd in widths[0] if dd in widths[1]]
+    if not common:
+        raise ValueError("k_codes and v_codes rows belong to different d")
+    d = common[0]
+    if index is None:
+        index = torch.full((batch, hkv, keep), -1, dtype=torch.int32, device=dev)
+    if out_lens is None:
+        out_lens = torch.empty(batch, dtype=torch.int32, device=dev)
+    if out_mass is None:
+        out_mass = torch.zeros(batch, hkv, keep, dtype=torch.float32, device=dev)
+    if out is None:
+        out = [torch.zeros(batch, keep, *t_.shape[2:], dtype=t_.dtype, device=dev)
+               for t_ in (k_codes, k_norms, v_codes, v_norms)]
+    _dev_tensor(index, "index", (torch.int32,))
+    _dev_tensor(out_lens, "out_lens", (torch.int32,))
+    _dev_tensor(out_mass, "out_mass", (torch.float32,))
+    if index.numel() != batch * hkv * keep or out_mass.numel() != batch * hkv * keep or out_lens.numel() != batch:
+        raise ValueError("index / out_mass / out_lens have the wrong size")
+    for o, t_ in zip(out, (k_codes, k_norms, v_codes, v_norms)):
+        _dev_tensor(o, "out", (t_.dtype,))
+        if o.numel() != (t_.numel() // cap * keep if cap else o.numel()):
+            raise ValueError("out has the wrong size")
+    if lens is not None:
+        _dev_tensor(lens, "lens", (torch.int32,))
+        if lens.numel() != batch:
+            raise ValueError("lens must hold one length per sequence")
+    with _on_device(mass, lens, k_codes, k_norms, v_codes, v_norms, index, out_lens, out_mass, *out):
+        _check(lib().rrq_evict(_ptr(mass), batch, hkv, cap, _ptr(lens), keep, sink, recent, d, widths[0][d],
+                               widths[1][d], _ptr(k_codes), _ptr(k_norms), _ptr(v_codes), _ptr(v_norms),
+                               _ptr(index), _ptr(out_lens), _ptr(out_mass), _ptr(out[0]), _ptr(out[1]),
+                               _ptr(out[2]), _ptr(out[3]), _stream(mass)), "rrq_evict")
+    return (index, out_lens, out_mass, *out)
+
+
+def rrq_rope_frequencies(rot: int, base: float = 10000.0, schedule: str = "none", stretch: float = 1.0,
+                         original: float = 8192.0, fast: float = 32.0, slow: float = 1.0):
+    """(frequencies float64 [rot/2] in radians per position, factor on cos and sin) of a
+    rotary schedule: 'none', 'linear', 'ntk' or 'yarn'.  Host only."""
+    out = np.zeros(max(rot // 2, 1), dtype=np.float64)
+    factor = ctypes.c_double(0.0)
+    _check(lib().rrq_rope_frequencies(ROPE_SCHEDULES[schedule], rot, base, stretch, original, fast, slow,
+                                      _vp(out.ctypes.data), _vp(ctypes.addressof(factor))),
+           "rrq_rope_frequencies")
+    return out, factor.value
+
+
+def rrq_rope(x: torch.Tensor, positions: torch.Tensor, freqs, interleaved: bool = False,
+             factor: float = 1.0, inverse: bool = False, out=None):
+    """Rotary positions of x [n, heads, d] at int64 positions [n]: the first 2*len(freqs)
+    coordinates of every vector turned, the rest copied; ``inverse`` applies the transposed
+    map (the gradient with respect to x).  ``out`` may be ``x``."""
+    _dev_tensor(x, "x", DTYPE_CODE)
+    if x.dim() != 3:
+        raise ValueError("x must be [n, heads, d]")
+    n, heads, d = x.shape
+    _dev_tensor(positions, "positions", (torch.int64,))
+    if positions.numel() != n:
+        raise ValueError("positions must hold one position per token")
+    fr = np.ascontiguousarray(np.asarray(freqs, dtype=np.float64))
+    if out is None:
+        out = torch.empty_like(x)
+    _dev_tensor(out, "out", (x.dtype,))
+    if out.numel() != x.numel():
+        raise ValueError("out has the wrong size")
+    with _on_device(x, positions, out):
+        _check(lib().rrq_rope(_ptr(x), DTYPE_CODE[x.dtype], n, heads, d, 2 * fr.size, int(bool(interleaved)),
+                              _ptr(positions), _vp(fr.ctypes.data), float(factor), int(bool(inverse)),
+                              _ptr(out), _stream(x)), "rrq_rope")
+    return out

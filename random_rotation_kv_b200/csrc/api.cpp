@@ -9,7 +9,10 @@
 
 #include "rrq.h"
 #include "attention.h"
+#include "attention_shared.h"
+#include "evict.h"
 #include "ggml_blocks.h"
+#include "rope.h"
 #include "scores_qjl.h"
 #include "rrq_params.h"
 
@@ -401,6 +404,234 @@ int rrq_attention_decode(const void* q, int hq, const uint8_t* k_codes, const fl
                                       (size_t(hkv) * 4 + 255) / 256 * 256);
   const cudaError_t e = rrq::launch_attention_decode(a, as_stream(stream));
   return e == cudaErrorNotSupported ? RRQ_ERR_UNSUPPORTED : status_of(e);
+}
+
+namespace {
+// The shape of a shared-prefix attention call: RRQ_OK with the schedule in *a, or the status to return.
+int shared_shape(int64_t batch, int hq, int hkv, int d, int64_t prefix, int64_t tail_cap,
+                 rrq::SharedArgs* a) {
+  if (batch < 0 || prefix < 0 || tail_cap < 0 || hq < 1 || hkv < 1 || hq % hkv != 0 || !d_ok(d))
+    return RRQ_ERR_INVALID;
+  *a = rrq::SharedArgs{};
+  a->batch = batch;
+  a->hq = hq;
+  a->hkv = hkv;
+  a->d = d;
+  a->prefix = prefix;
+  a->cap = tail_cap;
+  return rrq::attention_shared_plan(a) ? RRQ_OK : RRQ_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+size_t rrq_attention_shared_workspace_bytes(int64_t batch, int hq, int hkv, int d, int64_t prefix,
+                                            int64_t tail_cap) {
+  rrq::SharedArgs a;
+  if (batch < 1 || shared_shape(batch, hq, hkv, d, prefix, tail_cap, &a) != RRQ_OK) return 0;
+  return rrq::attention_shared_layout(&a, nullptr);
+}
+
+int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,
+                         const uint8_t* pk_codes, const float* pk_norms, const uint8_t* pv_codes,
+                         const float* pv_norms, int64_t prefix, const uint8_t* tk_codes,
+                         const float* tk_norms, const uint8_t* tv_codes, const float* tv_norms,
+                         int64_t tail_cap, const int32_t* tail_lens, int hkv, int d, int k_bits,
+                         uint64_t k_seed, const float* k_codebook, int v_bits, uint64_t v_seed,
+                         const float* v_codebook, float scale, void* workspace,
+                         size_t workspace_bytes, void* out, void* stream) {
+  if (!dtype_ok(q_dtype) || !bits_ok(k_bits) || !bits_ok(v_bits) || !std::isfinite(scale))
+    return RRQ_ERR_INVALID;
+  rrq::SharedArgs a;
+  const int shape = shared_shape(batch, hq, hkv, d, prefix, tail_cap, &a);
+  if (shape == RRQ_ERR_INVALID) return shape;
+  if (!arr_ok(q, batch, 16) || !arr_ok(out, batch, 16)) return RRQ_ERR_INVALID;
+  if (!arr_ok(pk_codes, prefix, 16) || !arr_ok(pk_norms, prefix, 4) || !arr_ok(pv_codes, prefix, 16) ||
+      !arr_ok(pv_norms, prefix, 4))
+    return RRQ_ERR_INVALID;
+  const int64_t tails = batch > 0 ? tail_cap : 0;
+  if (!arr_ok(tk_codes, tails, 16) || !arr_ok(tk_norms, tails, 4) || !arr_ok(tv_codes, tails, 16) ||
+      !arr_ok(tv_norms, tails, 4) || !arr_ok(tail_lens, tails, 4))
+    return RRQ_ERR_INVALID;
+  rrq::QuantParams pk, pv;
+  if (make_params(k_bits, k_codebook, k_seed, d, &pk) != RRQ_OK ||
+      make_params(v_bits, v_codebook, v_seed, d, &pv) != RRQ_OK)
+    return RRQ_ERR_INVALID;
+  if (shape != RRQ_OK || q_dtype == RRQ_F32) return RRQ_ERR_UNSUPPORTED;
+  if (batch == 0) return RRQ_OK;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < rrq::attention_shared_layout(&a, workspace))
+    return RRQ_ERR_INVALID;
+  a.q = q;
+  a.out = out;
+  a.bf16 = q_dtype == RRQ_BF16;
+  a.k_codes[0] = pk_codes;
+  a.k_codes[1] = tk_codes;
+  a.k_norms[0] = pk_norms;
+  a.k_norms[1] = tk_norms;
+  a.v_codes[0] = pv_codes;
+  a.v_codes[1] = tv_codes;
+  a.v_norms[0] = pv_norms;
+  a.v_norms[1] = tv_norms;
+  a.lens = tail_cap > 0 ? tail_lens : nullptr;
+  a.k_bits = k_bits;
+  a.v_bits = v_bits;
+  a.k_seed = k_seed;
+  a.v_seed = v_seed;
+  a.kscale = static_cast<float>(double(scale) * 1.4426950408889634074 / d);
+  std::memcpy(a.k_levels, pk.levels, sizeof(a.k_levels));
+  std::memcpy(a.v_levels, pv.levels, sizeof(a.v_levels));
+  return status_of(rrq::launch_attention_shared(a, as_stream(stream)));
+}
+
+int rrq_attention_mass(const float* scores, int64_t batch, int hq, int hkv, int64_t T,
+                       const int32_t* lens, float decay, const float* mass, float* out,
+                       void* stream) {
+  if (batch < 0 || T < 0 || T > INT32_MAX || hq < 1 || hkv < 1 || hq % hkv != 0 || !std::isfinite(decay))
+    return RRQ_ERR_INVALID;
+  const int64_t n = batch > 0 ? T : 0;
+  if (!arr_ok(scores, n, 4) || !aligned(lens, 4) || !aligned(mass, 4) || !arr_ok(out, n, 4))
+    return RRQ_ERR_INVALID;
+  if (batch > INT32_MAX / hkv) return RRQ_ERR_INVALID;
+  if (n == 0) return RRQ_OK;
+  rrq::MassArgs a;
+  a.scores = scores;
+  a.lens = lens;
+  a.mass = mass;
+  a.out = out;
+  a.batch = batch;
+  a.T = T;
+  a.hkv = hkv;
+  a.group = hq / hkv;
+  a.decay = decay;
+  return status_of(rrq::launch_attention_mass(a, as_stream(stream)));
+}
+
+int rrq_evict(const float* mass, int64_t batch, int hkv, int64_t cap, const int32_t* lens,
+              int64_t keep, int64_t sink, int64_t recent, int d, int k_bits, int v_bits,
+              const uint8_t* k_codes, const float* k_norms, const uint8_t* v_codes,
+              const float* v_norms, int32_t* index, int32_t* out_lens, float* out_mass,
+              uint8_t* ok_codes, float* ok_norms, uint8_t* ov_codes, float* ov_norms, void* stream) {
+  if (batch < 0 || cap < 0 || cap > INT32_MAX || hkv < 1 || keep < 1 || sink < 0 || recent < 0 ||
+      sink > keep || recent > keep - sink || keep > INT32_MAX || !d_ok(d) || !bits_ok(k_bits) ||
+      !bits_ok(v_bits))
+    return RRQ_ERR_INVALID;
+  const int64_t n = batch > 0 ? cap : 0;
+  if (!arr_ok(mass, n, 4) || !aligned(lens, 4) || !arr_ok(k_codes, n, 16) || !arr_ok(k_norms, n, 4) ||
+      !arr_ok(v_codes, n, 16) || !arr_ok(v_norms, n, 4))
+    return RRQ_ERR_INVALID;
+  if (!arr_ok(index, n, 4) || !arr_ok(out_lens, batch, 4) || !aligned(out_mass, 4) ||
+      !arr_ok(ok_codes, n, 16) || !arr_ok(ok_norms, n, 4) || !arr_ok(ov_codes, n, 16) ||
+      !arr_ok(ov_norms, n, 4))
+    return RRQ_ERR_INVALID;
+  if (batch > INT32_MAX / hkv) return RRQ_ERR_INVALID;
+  if (batch == 0) return RRQ_OK;
+  if (cap == 0) return status_of(cudaMemsetAsync(out_lens, 0, size_t(batch) * 4, as_stream(stream)));
+  rrq::EvictArgs a;
+  a.mass = mass;
+  a.lens = lens;
+  a.k_codes = k_codes;
+  a.v_codes = v_codes;
+  a.k_norms = k_norms;
+  a.v_norms = v_norms;
+  a.index = index;
+  a.out_lens = out_lens;
+  a.out_mass = out_mass;
+  a.ok_codes = ok_codes;
+  a.ov_codes = ov_codes;
+  a.ok_norms = ok_norms;
+  a.ov_norms = ov_norms;
+  a.batch = batch;
+  a.cap = cap;
+  a.keep = keep;
+  a.sink = sink;
+  a.recent = recent;
+  a.hkv = hkv;
+  a.k_row = d * k_bits / 8;
+  a.v_row = d * v_bits / 8;
+  return status_of(rrq::launch_evict(a, as_stream(stream)));
+}
+
+int rrq_rope_frequencies(int schedule, int rot, double base, double stretch, double original,
+                         double fast, double slow, double* freqs, double* factor) {
+  if (rot < 2 || rot > 2 * rrq::kRopeMaxPairs || rot % 2 != 0 || freqs == nullptr || factor == nullptr ||
+      !std::isfinite(base) || !(base > 1.0) || !std::isfinite(stretch) || !(stretch >= 1.0))
+    return RRQ_ERR_INVALID;
+  if (schedule < RRQ_ROPE_NONE || schedule > RRQ_ROPE_YARN) return RRQ_ERR_INVALID;
+  if (schedule == RRQ_ROPE_YARN &&
+      (!std::isfinite(original) || !(original > 0.0) || !std::isfinite(fast) || !(slow > 0.0) || !(fast >= slow)))
+    return RRQ_ERR_INVALID;
+  const double two_pi = 6.283185307179586476925286766559;
+  *factor = schedule == RRQ_ROPE_YARN ? 0.1 * std::log(stretch) + 1.0 : 1.0;
+  if (schedule == RRQ_ROPE_NTK && rot > 2) base *= std::pow(stretch, double(rot) / (rot - 2));
+  auto turns = [&](double n) { return rot * std::log(original / (n * two_pi)) / (2.0 * std::log(base)); };
+  const bool yarn = schedule == RRQ_ROPE_YARN;
+  const double lo = yarn ? std::fmax(std::floor(turns(fast)), 0.0) : 0.0;
+  const double hi = yarn ? std::fmin(std::ceil(turns(slow)), double(rot - 1)) : 0.0;
+  for (int i = 0; i < rot / 2; ++i) {
+    const double theta = std::pow(base, -2.0 * i / rot);
+    if (schedule == RRQ_ROPE_LINEAR) {
+      freqs[i] = theta / stretch;
+    } else if (yarn) {
+      const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+      freqs[i] = theta * (1.0 - r) + theta / stretch * r;
+    } else {
+      freqs[i] = theta;
+    }
+  }
+  return RRQ_OK;
+}
+
+namespace {
+// Radians per position -> turns per position modulo one, in units of 2^-64 (nearest),
+// for |f| < 2^31: the 53-bit significand times 2^192/2π (three 64-bit limbs, the
+// binary digits of 1/2π), shifted into place, so no digit of the fraction is lost to
+// the whole turns before it.
+uint64_t turns_of(double f) {
+  static const uint64_t kInvTwoPi[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
+  int ex = 0;
+  const double m = std::frexp(std::fabs(f), &ex);  // |f| = m·2^ex, 0.5 ≤ m < 1
+  const uint64_t sig = static_cast<uint64_t>(std::ldexp(m, 53));  // |f| = sig·2^(ex − 53)
+  uint64_t limb[6] = {0, 0, 0, 0, 0, 0};
+  unsigned __int128 carry = 0;
+  for (int k = 0; k < 3; ++k) {
+    carry += static_cast<unsigned __int128>(sig) * kInvTwoPi[k];
+    limb[k] = static_cast<uint64_t>(carry);
+    carry >>= 64;
+  }
+  limb[3] = static_cast<uint64_t>(carry);
+  const int shift = 128 + 53 - ex;  // ≥ 150
+  if (shift > 64 * 4) return 0;     // less than half a unit
+  const int w = shift / 64, b = shift % 64;
+  uint64_t u = b ? (limb[w] >> b) | (limb[w + 1] << (64 - b)) : limb[w];
+  u += b ? (limb[w] >> (b - 1)) & 1u : limb[w - 1] >> 63;  // to nearest
+  return f < 0 ? 0 - u : u;
+}
+}  // namespace
+
+int rrq_rope(const void* x, int dtype, int64_t n, int heads, int d, int rot, int interleaved,
+             const int64_t* positions, const double* freqs, double factor, int inverse, void* y,
+             void* stream) {
+  if (n < 0 || heads < 1 || !d_ok(d) || !dtype_ok(dtype) || rot < 2 || rot > d || rot % 2 != 0 ||
+      (interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1) || freqs == nullptr ||
+      !std::isfinite(static_cast<float>(factor)))
+    return RRQ_ERR_INVALID;
+  if (!arr_ok(x, n, 16) || !arr_ok(y, n, 16) || !arr_ok(positions, n, 8)) return RRQ_ERR_INVALID;
+  rrq::RopeArgs a;
+  for (int i = 0; i < rot / 2; ++i) {
+    if (!(std::fabs(freqs[i]) < 2147483648.0)) return RRQ_ERR_INVALID;
+    a.turns[i] = turns_of(freqs[i]);
+  }
+  if (n == 0) return RRQ_OK;
+  a.x = x;
+  a.y = y;
+  a.positions = positions;
+  a.n = n;
+  a.heads = heads;
+  a.d = d;
+  a.rot = rot;
+  a.interleaved = interleaved;
+  a.cos_factor = static_cast<float>(factor);
+  a.sin_factor = inverse ? -a.cos_factor : a.cos_factor;
+  return status_of(rrq::launch_rope(a, dtype, as_stream(stream)));
 }
 
 int rrq_q4_0_rot(const void* x, int x_dtype, int64_t n, int d, uint64_t seed, int rotate,

@@ -1,0 +1,297 @@
+// attention_shared.cu — one decode step of attention for a batch of sequences over a
+// shared quantised prefix and a private quantised tail each.
+//
+// With g the kv head of query head h, over the prefix and then the sequence's tail:
+//     out = Σ_t p_t·v̂_t,   p = softmax(scale·⟨q, k̂_t⟩),   k̂ = Πᵀ(ν/√d·c[code]),
+// and Πᵀ = D·H/√d, so with q' = scale·log2 e/d · H·D·q the base-2 score is
+// x_t = ν_t·⟨q', c[code_t]⟩, the values are summed in their rotated domain and
+// rotated back once per row: out = D·H·(Σ 2^{x_t − m}·ν_t·c[code_t]) / (d·Σ 2^{x_t − m}).
+//
+// Three launches: the queries are rotated (and the tails' tiles counted), every CTA walks
+// its range of the line of tiles (attention_shared.h) and leaves a partial state
+// (m, Σ 2^{x − m}, Σ 2^{x − m}·ν·c) per unit, and one warp per query row merges its parts
+// and rotates back.  No CTA waits for another, and nothing depends on the order in which
+// they run.
+#include <cmath>
+
+#include "attention_shared.cuh"
+
+namespace rrq {
+namespace {
+
+constexpr int kMinTiles = 2;  // tiles per range at least: a state costs about as much as a tile
+
+// Walsh–Hadamard transform over a warp's row: coordinate 32·i + lane in v[i].
+template <int N> __device__ __forceinline__ void fwht_row(float (&v)[N], int lane) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float o = __shfl_xor_sync(kFull, v[i], m);
+      v[i] = lane & m ? o - v[i] : v[i] + o;
+    }
+#pragma unroll
+  for (int m = 1; m < N; m <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(i & m)) {
+        const float x = v[i], y = v[i | m];
+        v[i] = x + y;
+        v[i | m] = x - y;
+      }
+}
+
+// ---- queries rotated, one warp per row; block 0 also lays out the line of tiles
+template <int D>
+__global__ void __launch_bounds__(256) shared_prepare_kernel(const SharedArgs a) {
+  constexpr int N = D / 32;
+  __shared__ int s_sum[256];
+  pdl_release();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x == 0) {
+    int before = 0;
+    for (int64_t b0 = 0; b0 < a.batch; b0 += 256) {
+      const int64_t b = b0 + tid;
+      const int mine = b < a.batch ? (shared_tail_len(a, b) + a.tile - 1) / a.tile : 0;
+      s_sum[tid] = mine;
+      __syncthreads();
+      for (int o = 1; o < 256; o <<= 1) {
+        const int v = tid >= o ? s_sum[tid - o] : 0;
+        __syncthreads();
+        s_sum[tid] += v;
+        __syncthreads();
+      }
+      if (b < a.batch) a.head[kHeadTails + b] = before + s_sum[tid] - mine;
+      before += s_sum[255];
+      __syncthreads();
+    }
+    if (tid == 0) {
+      a.head[kHeadTails + a.batch] = before;
+      const int total = a.hkv * (a.row_tiles * a.ptiles + before);
+      const int per = (total + a.grid - 1) / a.grid;
+      a.head[0] = total;
+      a.head[1] = per < kMinTiles ? kMinTiles : per;
+    }
+  }
+  const int64_t row = int64_t(blockIdx.x) * 8 + warp;  // b·hq + h
+  if (row >= a.batch * a.hq) return;
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t at = row * D + 32 * i + lane;
+    const float x = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at])
+                           : __half2float(static_cast<const __half*>(a.q)[at]);
+    v[i] = sign_bit(a.k_seed, 32 * i + lane) ? -x : x;
+  }
+  fwht_row(v, lane);
+  const int64_t b = row / a.hq;
+  const int h = int(row % a.hq), g = h / a.group;
+  float* dst = a.qrot + (int64_t(g) * a.rows + b * a.group + h % a.group) * D;
+#pragma unroll
+  for (int i = 0; i < N; ++i) dst[32 * i + lane] = v[i] * a.kscale;
+}
+
+// ---- partial states: 8 query rows at a time, one warp each, 32 tokens per step
+template <int D>
+__global__ void __launch_bounds__(256) shared_partial_kernel(const SharedArgs a) {
+  constexpr int N = D / 32, P = D + 1;
+  extern __shared__ float sm[];
+  float* s_kv = sm;             // [32][P] values of 32 tokens
+  float* s_q = sm + 32 * P;     // [8][D]
+  float* s_lev = s_q + 8 * D;   // [2][16]
+  pdl_release();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 16) s_lev[tid] = a.k_levels[tid];
+  else if (tid < 32) s_lev[tid] = a.v_levels[tid - 16];
+  const int range = blockIdx.x;
+  const int per = a.head[1], total = a.head[0];
+  int64_t start = int64_t(range) * per;
+  const int end = int(start + per < total ? start + per : total);
+  for (int pos = int(start < total ? start : total); pos < end;) {
+    const Segment s = segment_at(a, range, pos, end);
+    pos += s.tiles;
+    const int kv = s.part;
+    // 32 tokens' values (codes' levels, unscaled) into s_kv; tokens past the end repeat the last
+    auto load = [&](const uint8_t* codes, int bits, const float* lev, int64_t t) {
+      for (int i = tid; i < 32 * (D / 8); i += 256) {
+        const int tok = i / (D / 8), o = i % (D / 8);
+        const int64_t tt = t + tok < s.t1 ? t + tok : s.t1 - 1;
+        const uint8_t* p = codes + ((s.token_base + tt) * a.hkv + s.g) * (D * bits / 8) + o * bits;
+        uint32_t w = 0;
+        for (int k = 0; k < bits; ++k) w |= uint32_t(p[k]) << (8 * k);
+        w = octet_nibbles(w, bits);
+        for (int j = 0; j < 8; ++j) s_kv[tok * P + 8 * o + j] = lev[(w >> (4 * j)) & 15u];
+      }
+    };
+    for (int r0 = 0; r0 < s.nrows; r0 += 8) {
+      const int r = r0 + warp;
+      const bool live = r < s.nrows;
+      const float* q = a.qrot + (int64_t(s.g) * a.rows + s.row0 + (live ? r : 0)) * D;
+      for (int i = lane; i < D; i += 32) s_q[warp * D + i] = q[i];
+      float m = -INFINITY, l = 0.f, acc[N];
+      for (int i = 0; i < N; ++i) acc[i] = 0.f;
+      for (int64_t t = s.t0; t < s.t1; t += 32) {
+        __syncthreads();
+        load(a.k_codes[kv], a.k_bits, s_lev, t);
+        __syncthreads();
+        const bool valid = t + lane < s.t1;
+        const int64_t row = (s.token_base + (valid ? t + lane : s.t1 - 1)) * a.hkv + s.g;
+        float x = 0.f;
+        for (int i = 0; i < D; ++i) x = fmaf(s_q[warp * D + i], s_kv[lane * P + i], x);
+        x = valid ? x * a.k_norms[kv][row] : -INFINITY;
+        const float nu = a.v_norms[kv][row];
+        float mx = x;
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        const float mn = fmaxf(m, mx), f = exp2f(m - mn);
+        const float p = valid ? exp2f(x - mn) : 0.f;
+        m = mn;
+        l = l * f + p;
+        for (int i = 0; i < N; ++i) acc[i] *= f;
+        const float w = valid ? p * nu : 0.f;
+        __syncthreads();
+        load(a.v_codes[kv], a.v_bits, s_lev + 16, t);
+        __syncthreads();
+        for (int k = 0; k < 32; ++k) {
+          const float wk = __shfl_sync(kFull, w, k);
+          for (int i = 0; i < N; ++i) acc[i] = fmaf(wk, s_kv[k * P + 32 * i + lane], acc[i]);
+        }
+      }
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+      if (live) {
+        if (lane == 0) a.stats[s.state + r] = make_float2(m, l);
+        for (int i = 0; i < N; ++i) a.acc[(s.state + r) * D + 32 * i + lane] = acc[i];
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---- one warp per query row: its parts merged, rotated back, rounded to the output type
+template <int D>
+__global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
+  constexpr int N = D / 32;
+  pdl_release();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);  // b·hq + h
+  if (row >= a.batch * a.hq) return;
+  const int64_t b = row / a.hq;
+  const int h = int(row % a.hq), g = h / a.group;
+  const int64_t r = b * a.group + h % a.group;
+  const int per = a.head[1];
+  const int ptotal = a.hkv * a.row_tiles * a.ptiles;
+  int np = 0, nt = 0;
+  if (a.ptiles > 0) {
+    const int first = (g * a.row_tiles + int(r / 128)) * a.ptiles;
+    np = (first + a.ptiles - 1) / per - first / per + 1;
+  }
+  const int* sums = a.head + kHeadTails;
+  const int tiles = sums[b + 1] - sums[b];
+  if (tiles > 0) {
+    const int first = ptotal + a.hkv * sums[b] + g * tiles;
+    nt = (first + tiles - 1) / per - first / per + 1;
+  }
+  auto state = [&](int i) {
+    const int p = i < np ? i : a.parts_p + (i - np);
+    return (int64_t(p) * a.hkv + g) * a.rows + r;
+  };
+  float m = -INFINITY;
+  for (int i = lane; i < np + nt; i += 32) m = fmaxf(m, a.stats[state(i)].x);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  float v[N], l = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  for (int i = 0; i < np + nt; ++i) {
+    const int64_t st = state(i);
+    const float2 ml = a.stats[st];
+    const float f = exp2f(ml.x - m);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = fmaf(a.acc[st * D + 32 * k + lane], f, v[k]);
+  }
+  fwht_row(v, lane);
+  const float inv = np + nt > 0 ? 1.f / (l * float(D)) : 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int c = 32 * k + lane;
+    const float y = np + nt > 0 ? (sign_bit(a.v_seed, c) ? -v[k] : v[k]) * inv : 0.f;
+    if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + c] = __float2bfloat16_rn(y);
+    else static_cast<__half*>(a.out)[row * D + c] = __float2half_rn(y);
+  }
+}
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms < 1 ? 1 : sms;
+}
+
+template <int D> cudaError_t launch_d(const SharedArgs& a, cudaStream_t stream) {
+  const int64_t rows = a.batch * a.hq;
+  const dim3 blocks(unsigned((rows + 7) / 8));
+  cudaError_t e = launch_pdl(shared_prepare_kernel<D>, blocks, dim3(256), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  constexpr size_t smem = (32 * (D + 1) + 8 * D + 32) * 4;
+  e = cudaFuncSetAttribute(shared_partial_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(shared_partial_kernel<D>, dim3(unsigned(a.grid)), dim3(256), smem, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(shared_merge_kernel<D>, blocks, dim3(256), 0, stream, a);
+}
+
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+bool attention_shared_plan(SharedArgs* a) {
+  a->group = a->hq / a->hkv;
+  if (a->group > 128) return false;
+  a->tile = a->d <= 128 ? 128 : 64;
+  const int64_t most = int64_t(1) << 30;  // 64-token tiles of all units
+  if (a->prefix / 64 >= most || a->cap / 64 >= most || a->batch >= most / a->hq) return false;
+  a->rows = a->batch * a->group;
+  a->row_tiles = int((a->rows + 127) / 128);
+  const int64_t pt = (a->prefix + a->tile - 1) / a->tile, tt = (a->cap + a->tile - 1) / a->tile;
+  const int64_t punits = int64_t(a->hkv) * a->row_tiles, tunits = int64_t(a->hkv) * a->batch;
+  if (tunits == 0) return true;  // no sequence: nothing runs
+  if (pt > most / punits || tt > most / tunits || punits * pt + tunits * tt >= most) return false;
+  a->ptiles = int(pt);
+  a->grid = sm_count();
+  const int64_t ptotal = punits * pt;
+  int64_t per = (ptotal + a->grid - 1) / a->grid;  // a range is never shorter
+  if (per < kMinTiles) per = kMinTiles;
+  auto parts = [per](int64_t tiles) {
+    const int64_t p = tiles > 0 ? (tiles - 1) / per + 2 : 0;
+    return int(p < tiles ? p : tiles);
+  };
+  a->parts_p = parts(pt);
+  a->parts_t = parts(tt);
+  return true;
+}
+
+size_t attention_shared_layout(SharedArgs* a, void* base) {
+  const size_t rows = size_t(a->rows) * size_t(a->hkv), parts = size_t(a->parts_p) + size_t(a->parts_t);
+  const size_t head = pad256((kHeadTails + size_t(a->batch) + 1) * 4);
+  const size_t q = pad256(rows * a->d * 4), st = pad256(parts * rows * 8);
+  uint8_t* p = static_cast<uint8_t*>(base);
+  if (p != nullptr) {
+    a->head = reinterpret_cast<int*>(p);
+    a->qrot = reinterpret_cast<float*>(p + head);
+    a->stats = reinterpret_cast<float2*>(p + head + q);
+    a->acc = reinterpret_cast<float*>(p + head + q + st);
+  }
+  return head + q + st + pad256(parts * rows * a->d * 4);
+}
+
+cudaError_t launch_attention_shared(const SharedArgs& a, cudaStream_t stream) {
+  switch (a.d) {
+    case 64: return launch_d<64>(a, stream);
+    case 128: return launch_d<128>(a, stream);
+    case 256: return launch_d<256>(a, stream);
+    default: return launch_d<512>(a, stream);
+  }
+}
+
+}  // namespace rrq

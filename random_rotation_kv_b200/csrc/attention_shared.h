@@ -1,0 +1,54 @@
+// attention_shared.h — arguments, schedule and launcher of attention for a batch over a
+// shared quantised prefix and private quantised tails (attention_shared.cu), called by
+// the C ABI (api.cpp).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "rrq_params.h"
+
+namespace rrq {
+
+// The cache is walked in tiles of `tile` tokens.  A unit is a run of tiles that one set
+// of query rows attends to: the prefix of kv head g with up to 128 rows (row tile rt),
+// or the tail of sequence b at kv head g with its `group` rows.  All units' tiles stand
+// in one line (prefix units first, then the tails by sequence and head), cut into
+// `grid` ranges of equal length: range c belongs to CTA c, and a unit that crosses
+// ranges leaves one partial state per range, merged at the end.
+struct SharedArgs {
+  const void* q;  // [batch × hq × d] fp16 or bf16
+  void* out;      // the same
+  int bf16;
+  const uint8_t* k_codes[2];  // prefix, tails
+  const uint8_t* v_codes[2];
+  const float* k_norms[2];
+  const float* v_norms[2];
+  const int32_t* lens;
+  int64_t batch, prefix, cap;
+  int hq, hkv, group, d;
+  int64_t rows;          // query rows of a kv head: batch × group, row b·group + j
+  int row_tiles;         // ⌈rows / 128⌉
+  int tile;              // tokens per tile
+  int ptiles;            // tiles of the prefix
+  int grid;              // ranges
+  int parts_p, parts_t;  // most ranges that share a prefix unit, a tail unit
+  int k_bits, v_bits;
+  uint64_t k_seed, v_seed;
+  float kscale;          // scale · log2 e / d
+  float k_levels[kMaxLevels], v_levels[kMaxLevels];
+  // workspace
+  int* head;      // [0] tiles in all, [1] tiles per range, [16 + b] tiles of the tails before b (one kv head)
+  float* qrot;    // rotated queries, row (g·rows + r), d values
+  float2* stats;  // (m, l) of part p, kv head g, row r at (p·hkv + g)·rows + r; prefix parts, then tail parts
+  float* acc;     // the same rows × d
+};
+
+// Fills the schedule's fields from batch, hq, hkv, d, prefix and cap for the current
+// device; false for a shape that is not supported (or an invalid one).
+bool attention_shared_plan(SharedArgs* a);
+// Bytes of the workspace of a planned call; with `base` also sets its pointers.
+size_t attention_shared_layout(SharedArgs* a, void* base);
+cudaError_t launch_attention_shared(const SharedArgs& a, cudaStream_t stream);
+
+}  // namespace rrq
