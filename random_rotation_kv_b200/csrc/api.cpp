@@ -479,7 +479,11 @@ int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,
   a.kscale = static_cast<float>(double(scale) * 1.4426950408889634074 / d);
   std::memcpy(a.k_levels, pk.levels, sizeof(a.k_levels));
   std::memcpy(a.v_levels, pv.levels, sizeof(a.v_levels));
-  return status_of(rrq::launch_attention_shared(a, as_stream(stream)));
+  // fp16 queries: a second fp16 part keeps what the rotation would lose; bf16 ones have less to lose
+  a.split = q_dtype == RRQ_F16 && d <= 128;
+  rrq::attention_shared_levels(&a, k_codebook == nullptr, v_codebook == nullptr);
+  const cudaError_t e = rrq::launch_attention_shared(a, as_stream(stream));
+  return e == cudaErrorNotSupported ? RRQ_ERR_UNSUPPORTED : status_of(e);
 }
 
 int rrq_attention_mass(const float* scores, int64_t batch, int hq, int hkv, int64_t T,

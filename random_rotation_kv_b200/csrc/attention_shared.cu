@@ -19,6 +19,7 @@
 namespace rrq {
 namespace {
 
+constexpr int kTcMaxD = 256;  // head sizes of the tensor-core kernel
 constexpr int kMinTiles = 2;  // tiles per range at least: a state costs about as much as a tile
 
 // Walsh–Hadamard transform over a warp's row: coordinate 32·i + lane in v[i].
@@ -87,9 +88,32 @@ __global__ void __launch_bounds__(256) shared_prepare_kernel(const SharedArgs a)
   fwht_row(v, lane);
   const int64_t b = row / a.hq;
   const int h = int(row % a.hq), g = h / a.group;
-  float* dst = a.qrot + (int64_t(g) * a.rows + b * a.group + h % a.group) * D;
+  const int64_t to = int64_t(g) * a.rows + b * a.group + h % a.group;
+  if constexpr (D > kTcMaxD) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) dst[32 * i + lane] = v[i] * a.kscale;
+    for (int i = 0; i < N; ++i) a.qrot[to * D + 32 * i + lane] = v[i] * a.kscale;
+  } else {
+    // fp16, the row's largest magnitude brought into [2^14, 2^15)
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] *= a.kscale;
+      big = fmaxf(big, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+    int e = int(__float_as_uint(big) >> 23) - 127;
+    if (e < -100) e = -100;
+    const float f = __uint_as_float(uint32_t(127 + 14 - e) << 23);
+    if (lane == 0) a.qexp[to] = __uint_as_float(uint32_t(127 + e - 14) << 23);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = v[i] * f;
+      const __half hi = __float2half_rn(x);
+      a.qh[to * D + 32 * i + lane] = hi;
+      if (a.split) a.ql[to * D + 32 * i + lane] = __float2half_rn(x - __half2float(hi));
+    }
+  }
 }
 
 // ---- partial states: 8 query rows at a time, one warp each, 32 tokens per step
@@ -212,7 +236,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
     for (int k = 0; k < N; ++k) v[k] = fmaf(a.acc[st * D + 32 * k + lane], f, v[k]);
   }
   fwht_row(v, lane);
-  const float inv = np + nt > 0 ? 1.f / (l * float(D)) : 0.f;
+  const float inv = np + nt > 0 ? 1.f / (l * float(D) * a.v_alpha) : 0.f;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int c = 32 * k + lane;
@@ -233,10 +257,14 @@ template <int D> cudaError_t launch_d(const SharedArgs& a, cudaStream_t stream) 
   const dim3 blocks(unsigned((rows + 7) / 8));
   cudaError_t e = launch_pdl(shared_prepare_kernel<D>, blocks, dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
-  constexpr size_t smem = (32 * (D + 1) + 8 * D + 32) * 4;
-  e = cudaFuncSetAttribute(shared_partial_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(shared_partial_kernel<D>, dim3(unsigned(a.grid)), dim3(256), smem, stream, a);
+  if constexpr (D > kTcMaxD) {
+    constexpr size_t smem = (32 * (D + 1) + 8 * D + 32) * 4;
+    e = cudaFuncSetAttribute(shared_partial_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(shared_partial_kernel<D>, dim3(unsigned(a.grid)), dim3(256), smem, stream, a);
+  } else {
+    e = launch_shared_tc(a, stream);
+  }
   if (e != cudaSuccess) return e;
   return launch_pdl(shared_merge_kernel<D>, blocks, dim3(256), 0, stream, a);
 }
@@ -271,18 +299,39 @@ bool attention_shared_plan(SharedArgs* a) {
   return true;
 }
 
+void attention_shared_levels(SharedArgs* a, bool default_k, bool default_v) {
+  // by bits: the factor of least mean square error over N(0,1) coordinates, from a search
+  // over all fp32 values in [1, 2): relative error 1e-10, 1e-7, 7e-6, 3.8e-5 (2e-4 unscaled)
+  static const float kBest[5] = {1.f, 0x1.1dc17p+0f, 0x1.fb2502p+0f, 0x1.24fd4ap+0f, 0x1.429a86p+0f};
+  auto alpha = [](const float* lev, int bits, bool dflt) {
+    float big = 0.f;
+    for (int k = 0; k < 1 << bits; ++k) big = std::fmax(big, std::fabs(lev[k]));
+    int e = 0;
+    std::frexp(big, &e);  // big in [2^(e − 1), 2^e)
+    return dflt ? kBest[bits] : std::ldexp(1.f, e < -99 ? 100 : 1 - e);
+  };
+  a->k_alpha = a->v_alpha = 1.f;
+  if (a->d > kTcMaxD) return;
+  a->k_alpha = alpha(a->k_levels, a->k_bits, default_k);
+  a->v_alpha = alpha(a->v_levels, a->v_bits, default_v);
+  a->kscale /= a->k_alpha;
+}
+
 size_t attention_shared_layout(SharedArgs* a, void* base) {
   const size_t rows = size_t(a->rows) * size_t(a->hkv), parts = size_t(a->parts_p) + size_t(a->parts_t);
   const size_t head = pad256((kHeadTails + size_t(a->batch) + 1) * 4);
-  const size_t q = pad256(rows * a->d * 4), st = pad256(parts * rows * 8);
+  const size_t q = pad256(rows * a->d * 4), qe = pad256(rows * 4), st = pad256(parts * rows * 8);
   uint8_t* p = static_cast<uint8_t*>(base);
   if (p != nullptr) {
     a->head = reinterpret_cast<int*>(p);
     a->qrot = reinterpret_cast<float*>(p + head);
-    a->stats = reinterpret_cast<float2*>(p + head + q);
-    a->acc = reinterpret_cast<float*>(p + head + q + st);
+    a->qh = reinterpret_cast<__half*>(p + head);
+    a->ql = a->qh + rows * a->d;
+    a->qexp = reinterpret_cast<float*>(p + head + q);
+    a->stats = reinterpret_cast<float2*>(p + head + q + qe);
+    a->acc = reinterpret_cast<float*>(p + head + q + qe + st);
   }
-  return head + q + st + pad256(parts * rows * a->d * 4);
+  return head + q + qe + st + pad256(parts * rows * a->d * 4);
 }
 
 cudaError_t launch_attention_shared(const SharedArgs& a, cudaStream_t stream) {

@@ -3,6 +3,7 @@
 // the C ABI (api.cpp).
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -35,11 +36,19 @@ struct SharedArgs {
   int parts_p, parts_t;  // most ranges that share a prefix unit, a tail unit
   int k_bits, v_bits;
   uint64_t k_seed, v_seed;
-  float kscale;          // scale · log2 e / d
+  float kscale;          // scale · log2 e / d (over k_alpha)
   float k_levels[kMaxLevels], v_levels[kMaxLevels];
+  // The tensor-core kernel's fp16 levels are rn(alpha · c): a power of two that brings the
+  // largest level into [1, 2), times, for the default codebooks, the factor in [1, 2)
+  // for which the rounded levels are nearest to the exact ones.
+  float k_alpha, v_alpha;
+  int split;             // queries as two fp16 parts
   // workspace
   int* head;      // [0] tiles in all, [1] tiles per range, [16 + b] tiles of the tails before b (one kv head)
-  float* qrot;    // rotated queries, row (g·rows + r), d values
+  float* qrot;    // rotated queries, row (g·rows + r), d values (d = 512), or in their place
+  __half* qh;     //   the same as fp16 times a power of two per row,
+  __half* ql;     //   what that rounding left, when split,
+  float* qexp;    //   and the power of two taken out
   float2* stats;  // (m, l) of part p, kv head g, row r at (p·hkv + g)·rows + r; prefix parts, then tail parts
   float* acc;     // the same rows × d
 };
@@ -47,8 +56,14 @@ struct SharedArgs {
 // Fills the schedule's fields from batch, hq, hkv, d, prefix and cap for the current
 // device; false for a shape that is not supported (or an invalid one).
 bool attention_shared_plan(SharedArgs* a);
+// Sets alpha (and divides kscale by it) from the levels; `default_k`, `default_v`: the
+// default codebook.
+void attention_shared_levels(SharedArgs* a, bool default_k, bool default_v);
 // Bytes of the workspace of a planned call; with `base` also sets its pointers.
 size_t attention_shared_layout(SharedArgs* a, void* base);
 cudaError_t launch_attention_shared(const SharedArgs& a, cudaStream_t stream);
+// The partial states on the tensor cores (d ≤ 256), between the two launches of
+// launch_attention_shared.  cudaErrorNotSupported where the layout cannot be had.
+cudaError_t launch_shared_tc(const SharedArgs& a, cudaStream_t stream);
 
 }  // namespace rrq
