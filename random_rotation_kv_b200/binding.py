@@ -9,7 +9,9 @@ path.  If ``librrq.so`` is missing the first call raises immediately.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -421,21 +423,37 @@ def rrq_qjl_matrix(seed: int, d: int, device=None) -> torch.Tensor:
     return t if device is None else t.to(device)
 
 
-def _on_device(first: torch.Tensor, *others) -> torch.cuda.device:
-    """Context in which `first`'s device is the current one (a no-op where it is already);
-    the other tensors must live there too."""
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and on {t.device}")
-    return torch.cuda.device(first.device)
+# ---- serving calls.  A decode step issues these every few microseconds, so they hand
+# plain integers to ctypes and ask torch for the raw stream.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_F32, _U8, _I32, _I64 = torch.float32, torch.uint8, torch.int32, torch.int64
 
 
-def _cache_part(codes, norms, lead, hkv, row, what):
-    """Checks one K or V array pair of `lead` × hkv rows of `row` bytes."""
-    _dev_tensor(codes, f"{what}_codes", (torch.uint8,))
-    _dev_tensor(norms, f"{what}_norms", (torch.float32,))
-    if norms.numel() != lead * hkv or codes.numel() != lead * hkv * row:
-        raise ValueError(f"{what}_codes / {what}_norms have the wrong size")
+def _need(t, name: str, dtype, numel: int, dev: int) -> int:
+    """Address of a contiguous CUDA tensor of `numel` elements on device `dev`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the first argument")
+    return t.data_ptr()
+
+
+def _call(name: str, dev: int, *args) -> None:
+    """The C entry point `name` on device `dev` (the current one for its duration)."""
+    fn = getattr(_lib or lib(), name)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status != RRQ_OK:
+        raise RRQError(status, name)
 
 
 def rrq_attention_shared(q: torch.Tensor, pk_codes, pk_norms, pv_codes, pv_norms, tk_codes, tk_norms,
@@ -457,45 +475,45 @@ def rrq_attention_shared(q: torch.Tensor, pk_codes, pk_norms, pv_codes, pv_norms
         raise ValueError("q must be [batch, hq, d]")
     if hkv < 1:
         raise ValueError("hkv must be at least 1")
-    batch, hq = q.shape[:2]
+    batch, hq, _ = q.shape
+    dev = q.get_device()
     prefix = cap = 0
+    pk = pkn = pv = pvn = tk = tkn = tv = tvn = tl = None
+    k_row, v_row = d * k_bits // 8, d * v_bits // 8
     if pk_codes is not None:
-        _dev_tensor(pk_norms, "pk_norms", (torch.float32,))
-        prefix = pk_norms.numel() // hkv
-        _cache_part(pk_codes, pk_norms, prefix, hkv, d * k_bits // 8, "pk")
-        _cache_part(pv_codes, pv_norms, prefix, hkv, d * v_bits // 8, "pv")
+        rows = pk_norms.numel()
+        prefix = rows // hkv
+        if prefix * hkv != rows:
+            raise ValueError("pk_norms must hold prefix*hkv values")
+        pk, pkn = _need(pk_codes, "pk_codes", _U8, rows * k_row, dev), _need(pk_norms, "pk_norms", _F32, rows, dev)
+        pv, pvn = _need(pv_codes, "pv_codes", _U8, rows * v_row, dev), _need(pv_norms, "pv_norms", _F32, rows, dev)
     if tk_codes is not None:
-        _dev_tensor(tk_norms, "tk_norms", (torch.float32,))
-        cap = tk_norms.numel() // (batch * hkv) if batch else 0
-        _cache_part(tk_codes, tk_norms, batch * cap, hkv, d * k_bits // 8, "tk")
-        _cache_part(tv_codes, tv_norms, batch * cap, hkv, d * v_bits // 8, "tv")
-        _dev_tensor(tail_lens, "tail_lens", (torch.int32,))
-        if tail_lens.numel() != batch:
-            raise ValueError("tail_lens must hold one length per sequence")
+        rows = tk_norms.numel()
+        cap = rows // (batch * hkv) if batch else 0
+        if cap * batch * hkv != rows:
+            raise ValueError("tk_norms must hold batch*cap*hkv values")
+        tk, tkn = _need(tk_codes, "tk_codes", _U8, rows * k_row, dev), _need(tk_norms, "tk_norms", _F32, rows, dev)
+        tv, tvn = _need(tv_codes, "tv_codes", _U8, rows * v_row, dev), _need(tv_norms, "tv_norms", _F32, rows, dev)
+        tl = _need(tail_lens, "tail_lens", _I32, batch, dev)
     if out is None:
         out = torch.empty_like(q)
-    _dev_tensor(out, "out", (q.dtype,))
-    if out.numel() != q.numel():
-        raise ValueError("out has the wrong size")
-    with _on_device(q, pk_codes, pk_norms, pv_codes, pv_norms, tk_codes, tk_norms, tv_codes, tv_norms,
-                    tail_lens, out, workspace):
-        if workspace is None:
-            workspace = torch.empty(rrq_attention_shared_workspace_bytes(batch, hq, hkv, d, prefix, cap),
-                                    dtype=torch.uint8, device=q.device)
-        _dev_tensor(workspace, "workspace", (torch.uint8,))
-        kc, vc = _HostFloats(k_codebook), _HostFloats(v_codebook)
-        _check(lib().rrq_attention_shared(
-            _ptr(q), DTYPE_CODE[q.dtype], batch, hq, _ptr(pk_codes), _ptr(pk_norms), _ptr(pv_codes),
-            _ptr(pv_norms), prefix, _ptr(tk_codes), _ptr(tk_norms), _ptr(tv_codes), _ptr(tv_norms), cap,
-            _ptr(tail_lens), hkv, d, k_bits, k_seed, kc.ptr, v_bits, v_seed, vc.ptr, float(scale),
-            _ptr(workspace), workspace.numel(), _ptr(out), _stream(q)), "rrq_attention_shared")
+    to = _need(out, "out", q.dtype, q.numel(), dev)
+    if workspace is None:
+        with torch.cuda.device(dev) if dev != torch.cuda.current_device() else contextlib.nullcontext():
+            need = rrq_attention_shared_workspace_bytes(batch, hq, hkv, d, prefix, cap)
+        workspace = torch.empty(need, dtype=_U8, device=q.device)
+    size = workspace.numel()
+    ws = _need(workspace, "workspace", _U8, size, dev)
+    kc, vc = _HostFloats(k_codebook), _HostFloats(v_codebook)
+    _call("rrq_attention_shared", dev, q.data_ptr(), DTYPE_CODE[q.dtype], batch, hq, pk, pkn, pv, pvn, prefix, tk,
+          tkn, tv, tvn, cap, tl, hkv, d, k_bits, k_seed, kc.ptr, v_bits, v_seed, vc.ptr, scale, ws, size, to)
     return out
 
 
 def rrq_attention_shared_workspace_bytes(batch: int, hq: int, hkv: int, d: int, prefix: int,
                                          tail_cap: int) -> int:
     """Workspace bytes rrq_attention_shared needs on the current device."""
-    return int(lib().rrq_attention_shared_workspace_bytes(batch, hq, hkv, d, prefix, tail_cap))
+    return (_lib or lib()).rrq_attention_shared_workspace_bytes(batch, hq, hkv, d, prefix, tail_cap)
 
 
 def rrq_attention_mass(scores: torch.Tensor, hkv: int, mass=None, lens=None, decay: float = 1.0, out=None):
@@ -505,30 +523,33 @@ def rrq_attention_mass(scores: torch.Tensor, hkv: int, mass=None, lens=None, dec
 
     ``lens``: int32 [batch] on the device; tokens behind a sequence's length keep their
     mass.  ``mass``: the sums so far, zeros when not given.  ``out`` may be ``mass``."""
-    _dev_tensor(scores, "scores", (torch.float32,))
-    if scores.dim() not in (2, 3):
+    _dev_tensor(scores, "scores", (_F32,))
+    shape = scores.shape
+    if len(shape) not in (2, 3):
         raise ValueError("scores must be [batch, hq, T] or [hq, T]")
-    batch = scores.shape[0] if scores.dim() == 3 else 1
-    hq, t_len = scores.shape[-2:]
     if hkv < 1:
         raise ValueError("hkv must be at least 1")
+    batch = shape[0] if len(shape) == 3 else 1
+    hq, t_len = shape[-2:]
+    dev = scores.get_device()
     if out is None:
-        out = torch.empty(*scores.shape[:-2], hkv, t_len, dtype=torch.float32, device=scores.device)
-    _dev_tensor(out, "out", (torch.float32,))
-    if out.numel() != batch * hkv * t_len:
-        raise ValueError("out has the wrong size")
-    if mass is not None:
-        _dev_tensor(mass, "mass", (torch.float32,))
-        if mass.numel() != batch * hkv * t_len:
-            raise ValueError("mass has the wrong size")
-    if lens is not None:
-        _dev_tensor(lens, "lens", (torch.int32,))
-        if lens.numel() != batch:
-            raise ValueError("lens must hold one length per sequence")
-    with _on_device(scores, mass, lens, out):
-        _check(lib().rrq_attention_mass(_ptr(scores), batch, hq, hkv, t_len, _ptr(lens), float(decay),
-                                        _ptr(mass), _ptr(out), _stream(scores)), "rrq_attention_mass")
+        out = torch.empty((batch, hkv, t_len) if len(shape) == 3 else (hkv, t_len), dtype=_F32, device=scores.device)
+    n = batch * hkv * t_len
+    to = _need(out, "out", _F32, n, dev)
+    frm = None if mass is None else _need(mass, "mass", _F32, n, dev)
+    ln = None if lens is None else _need(lens, "lens", _I32, batch, dev)
+    _call("rrq_attention_mass", dev, scores.data_ptr(), batch, hq, hkv, t_len, ln, decay, frm, to)
     return out
+
+
+@functools.lru_cache(maxsize=None)
+def _row_widths(k_row: int, v_row: int):
+    """(d, k_bits, v_bits) of a cache with code rows of these sizes (the move depends on the
+    sizes alone, so any d that both fit will do)."""
+    for d in (64, 128, 256, 512):
+        if k_row * 8 % d == 0 and v_row * 8 % d == 0 and 1 <= k_row * 8 // d <= 4 and 1 <= v_row * 8 // d <= 4:
+            return d, k_row * 8 // d, v_row * 8 // d
+    raise ValueError(f"no d and bit widths give code rows of {k_row} and {v_row} bytes")
 
 
 def rrq_evict(mass: torch.Tensor, lens, keep: int, k_codes: torch.Tensor, k_norms: torch.Tensor,
@@ -542,60 +563,39 @@ def rrq_evict(mass: torch.Tensor, lens, keep: int, k_codes: torch.Tensor, k_norm
     [batch], out_mass [batch, hkv, keep], k_codes, k_norms, v_codes, v_norms of capacity
     `keep`).  ``out``: the four arrays of the new cache; entries behind a sequence's new
     length are left as they were (zeros, and -1 in index, where this call allocates)."""
-    _dev_tensor(mass, "mass", (torch.float32,))
+    _dev_tensor(mass, "mass", (_F32,))
     if mass.dim() != 3:
         raise ValueError("mass must be [batch, hkv, cap]")
     batch, hkv, cap = mass.shape
     if keep < 1:
         raise ValueError("keep must be at least 1")
-    dev = mass.device
     for t_, nm in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-        _dev_tensor(t_, nm, (torch.uint8,))
         if t_.dim() != 4 or t_.shape[:3] != (batch, cap, hkv):
             raise ValueError(f"{nm} must be [batch, cap, hkv, row bytes]")
     for t_, nm in ((k_norms, "k_norms"), (v_norms, "v_norms")):
-        _dev_tensor(t_, nm, (torch.float32,))
         if t_.shape != (batch, cap, hkv):
             raise ValueError(f"{nm} must be [batch, cap, hkv]")
-    # a row of 8·w bytes is d = 64·w codes of one bit, or any other d and width of that product
-    widths = []
-    for t_, nm in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-        row = t_.shape[3]
-        shapes = [(dd, row * 8 // dd) for dd in (64, 128, 256, 512) if row * 8 % dd == 0 and 1 <= row * 8 // dd <= 4]
-        if not shapes:
-            raise ValueError(f"{nm}: no d and bit width give rows of {row} bytes")
-        widths.append(dict(shapes))
-    common = [dd for dd in widths[0] if dd in widths[1]]
-    if not common:
-        raise ValueError("k_codes and v_codes rows belong to different d")
-    d = common[0]
+    dev, device = mass.get_device(), mass.device
+    k_row, v_row = k_codes.shape[3], v_codes.shape[3]
+    d, k_bits, v_bits = _row_widths(k_row, v_row)
     if index is None:
-        index = torch.full((batch, hkv, keep), -1, dtype=torch.int32, device=dev)
+        index = torch.full((batch, hkv, keep), -1, dtype=_I32, device=device)
     if out_lens is None:
-        out_lens = torch.empty(batch, dtype=torch.int32, device=dev)
+        out_lens = torch.empty(batch, dtype=_I32, device=device)
     if out_mass is None:
-        out_mass = torch.zeros(batch, hkv, keep, dtype=torch.float32, device=dev)
+        out_mass = torch.zeros(batch, hkv, keep, dtype=_F32, device=device)
     if out is None:
-        out = [torch.zeros(batch, keep, *t_.shape[2:], dtype=t_.dtype, device=dev)
+        out = [torch.zeros(batch, keep, *t_.shape[2:], dtype=t_.dtype, device=device)
                for t_ in (k_codes, k_norms, v_codes, v_norms)]
-    _dev_tensor(index, "index", (torch.int32,))
-    _dev_tensor(out_lens, "out_lens", (torch.int32,))
-    _dev_tensor(out_mass, "out_mass", (torch.float32,))
-    if index.numel() != batch * hkv * keep or out_mass.numel() != batch * hkv * keep or out_lens.numel() != batch:
-        raise ValueError("index / out_mass / out_lens have the wrong size")
-    for o, t_ in zip(out, (k_codes, k_norms, v_codes, v_norms)):
-        _dev_tensor(o, "out", (t_.dtype,))
-        if o.numel() != (t_.numel() // cap * keep if cap else o.numel()):
-            raise ValueError("out has the wrong size")
-    if lens is not None:
-        _dev_tensor(lens, "lens", (torch.int32,))
-        if lens.numel() != batch:
-            raise ValueError("lens must hold one length per sequence")
-    with _on_device(mass, lens, k_codes, k_norms, v_codes, v_norms, index, out_lens, out_mass, *out):
-        _check(lib().rrq_evict(_ptr(mass), batch, hkv, cap, _ptr(lens), keep, sink, recent, d, widths[0][d],
-                               widths[1][d], _ptr(k_codes), _ptr(k_norms), _ptr(v_codes), _ptr(v_norms),
-                               _ptr(index), _ptr(out_lens), _ptr(out_mass), _ptr(out[0]), _ptr(out[1]),
-                               _ptr(out[2]), _ptr(out[3]), _stream(mass)), "rrq_evict")
+    rows, new, slots = batch * cap * hkv, batch * keep * hkv, batch * hkv * keep
+    ln = None if lens is None else _need(lens, "lens", _I32, batch, dev)
+    _call("rrq_evict", dev, mass.data_ptr(), batch, hkv, cap, ln, keep, sink, recent, d, k_bits, v_bits,
+          _need(k_codes, "k_codes", _U8, rows * k_row, dev), _need(k_norms, "k_norms", _F32, rows, dev),
+          _need(v_codes, "v_codes", _U8, rows * v_row, dev), _need(v_norms, "v_norms", _F32, rows, dev),
+          _need(index, "index", _I32, slots, dev), _need(out_lens, "out_lens", _I32, batch, dev),
+          _need(out_mass, "out_mass", _F32, slots, dev), _need(out[0], "out[0]", _U8, new * k_row, dev),
+          _need(out[1], "out[1]", _F32, new, dev), _need(out[2], "out[2]", _U8, new * v_row, dev),
+          _need(out[3], "out[3]", _F32, new, dev))
     return (index, out_lens, out_mass, *out)
 
 
@@ -615,22 +615,17 @@ def rrq_rope(x: torch.Tensor, positions: torch.Tensor, freqs, interleaved: bool 
              factor: float = 1.0, inverse: bool = False, out=None):
     """Rotary positions of x [n, heads, d] at int64 positions [n]: the first 2*len(freqs)
     coordinates of every vector turned, the rest copied; ``inverse`` applies the transposed
-    map (the gradient with respect to x).  ``out`` may be ``x``."""
+    map (the gradient with respect to x).  ``freqs``: radians per position on the host
+    (float64, as rrq_rope_frequencies returns them).  ``out`` may be ``x``."""
     _dev_tensor(x, "x", DTYPE_CODE)
     if x.dim() != 3:
         raise ValueError("x must be [n, heads, d]")
     n, heads, d = x.shape
-    _dev_tensor(positions, "positions", (torch.int64,))
-    if positions.numel() != n:
-        raise ValueError("positions must hold one position per token")
-    fr = np.ascontiguousarray(np.asarray(freqs, dtype=np.float64))
+    dev = x.get_device()
+    fr = np.ascontiguousarray(freqs, dtype=np.float64)
     if out is None:
         out = torch.empty_like(x)
-    _dev_tensor(out, "out", (x.dtype,))
-    if out.numel() != x.numel():
-        raise ValueError("out has the wrong size")
-    with _on_device(x, positions, out):
-        _check(lib().rrq_rope(_ptr(x), DTYPE_CODE[x.dtype], n, heads, d, 2 * fr.size, int(bool(interleaved)),
-                              _ptr(positions), _vp(fr.ctypes.data), float(factor), int(bool(inverse)),
-                              _ptr(out), _stream(x)), "rrq_rope")
+    _call("rrq_rope", dev, x.data_ptr(), DTYPE_CODE[x.dtype], n, heads, d, 2 * fr.size, int(bool(interleaved)),
+          _need(positions, "positions", _I64, n, dev), fr.__array_interface__["data"][0], factor, int(bool(inverse)),
+          _need(out, "out", x.dtype, x.numel(), dev))
     return out

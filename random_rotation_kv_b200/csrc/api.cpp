@@ -116,15 +116,22 @@ void make_cell_table(const float* thr, int nthr, rrq::CellTable* ct) {
   ct->cells = 0;
 }
 
+// The levels of a codebook argument (NULL: the default), RRQ_ERR_INVALID unless ascending and finite.
+int copy_levels(int bits, const float* codebook, float* levels) {
+  const float* c = codebook ? codebook : default_codebooks().levels[bits];
+  for (int k = 0; k < 1 << bits; ++k) {
+    if (!std::isfinite(c[k])) return RRQ_ERR_INVALID;
+    if (k > 0 && !(c[k] > c[k - 1])) return RRQ_ERR_INVALID;
+    levels[k] = c[k];
+  }
+  return RRQ_OK;
+}
+
 int make_params(int bits, const float* codebook, uint64_t seed, int d, rrq::QuantParams* p) {
   std::memset(p, 0, sizeof(*p));
   const int L = 1 << bits;
-  const float* c = codebook ? codebook : default_codebooks().levels[bits];
-  for (int k = 0; k < L; ++k) {
-    if (!std::isfinite(c[k])) return RRQ_ERR_INVALID;
-    if (k > 0 && !(c[k] > c[k - 1])) return RRQ_ERR_INVALID;
-    p->levels[k] = c[k];
-  }
+  const float* c = p->levels;
+  if (copy_levels(bits, codebook, p->levels) != RRQ_OK) return RRQ_ERR_INVALID;
   for (int k = 0; k + 1 < L; ++k)
     p->thr[k] = static_cast<float>((static_cast<double>(c[k]) + static_cast<double>(c[k + 1])) * 0.5);
   int sym = 1;
@@ -451,9 +458,7 @@ int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,
   if (!arr_ok(tk_codes, tails, 16) || !arr_ok(tk_norms, tails, 4) || !arr_ok(tv_codes, tails, 16) ||
       !arr_ok(tv_norms, tails, 4) || !arr_ok(tail_lens, tails, 4))
     return RRQ_ERR_INVALID;
-  rrq::QuantParams pk, pv;
-  if (make_params(k_bits, k_codebook, k_seed, d, &pk) != RRQ_OK ||
-      make_params(v_bits, v_codebook, v_seed, d, &pv) != RRQ_OK)
+  if (copy_levels(k_bits, k_codebook, a.k_levels) != RRQ_OK || copy_levels(v_bits, v_codebook, a.v_levels) != RRQ_OK)
     return RRQ_ERR_INVALID;
   if (shape != RRQ_OK || q_dtype == RRQ_F32) return RRQ_ERR_UNSUPPORTED;
   if (batch == 0) return RRQ_OK;
@@ -477,8 +482,6 @@ int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,
   a.k_seed = k_seed;
   a.v_seed = v_seed;
   a.kscale = static_cast<float>(double(scale) * 1.4426950408889634074 / d);
-  std::memcpy(a.k_levels, pk.levels, sizeof(a.k_levels));
-  std::memcpy(a.v_levels, pv.levels, sizeof(a.v_levels));
   // fp16 queries: a second fp16 part keeps what the rotation would lose; bf16 ones have less to lose
   a.split = q_dtype == RRQ_F16 && d <= 128;
   rrq::attention_shared_levels(&a, k_codebook == nullptr, v_codebook == nullptr);

@@ -70,9 +70,10 @@ __global__ void __launch_bounds__(256) shared_prepare_kernel(const SharedArgs a)
     if (tid == 0) {
       a.head[kHeadTails + a.batch] = before;
       const int total = a.hkv * (a.row_tiles * a.ptiles + before);
-      const int per = (total + a.grid - 1) / a.grid;
+      const int64_t cost = int64_t(a.hkv) * (int64_t(a.row_tiles) * a.ptiles * a.pcost + int64_t(before) * a.tcost);
+      const int per = int((cost + a.grid - 1) / a.grid);
       a.head[0] = total;
-      a.head[1] = per < kMinTiles ? kMinTiles : per;
+      a.head[1] = per < a.min_cost ? a.min_cost : per;
     }
   }
   const int64_t row = int64_t(blockIdx.x) * 8 + warp;  // b·hq + h
@@ -130,10 +131,9 @@ __global__ void __launch_bounds__(256) shared_partial_kernel(const SharedArgs a)
   if (tid < 16) s_lev[tid] = a.k_levels[tid];
   else if (tid < 32) s_lev[tid] = a.v_levels[tid - 16];
   const int range = blockIdx.x;
-  const int per = a.head[1], total = a.head[0];
-  int64_t start = int64_t(range) * per;
-  const int end = int(start + per < total ? start + per : total);
-  for (int pos = int(start < total ? start : total); pos < end;) {
+  int pos, end;
+  range_tiles(a, range, &pos, &end);
+  while (pos < end) {
     const Segment s = segment_at(a, range, pos, end);
     pos += s.tiles;
     const int kv = s.part;
@@ -204,18 +204,17 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
   const int64_t b = row / a.hq;
   const int h = int(row % a.hq), g = h / a.group;
   const int64_t r = b * a.group + h % a.group;
-  const int per = a.head[1];
   const int ptotal = a.hkv * a.row_tiles * a.ptiles;
   int np = 0, nt = 0;
   if (a.ptiles > 0) {
     const int first = (g * a.row_tiles + int(r / 128)) * a.ptiles;
-    np = (first + a.ptiles - 1) / per - first / per + 1;
+    np = range_of(a, first + a.ptiles - 1) - range_of(a, first) + 1;
   }
   const int* sums = a.head + kHeadTails;
   const int tiles = sums[b + 1] - sums[b];
   if (tiles > 0) {
     const int first = ptotal + a.hkv * sums[b] + g * tiles;
-    nt = (first + tiles - 1) / per - first / per + 1;
+    nt = range_of(a, first + tiles - 1) - range_of(a, first) + 1;
   }
   auto state = [&](int i) {
     const int p = i < np ? i : a.parts_p + (i - np);
@@ -277,25 +276,30 @@ bool attention_shared_plan(SharedArgs* a) {
   a->group = a->hq / a->hkv;
   if (a->group > 128) return false;
   a->tile = a->d <= 128 ? 128 : 64;
-  const int64_t most = int64_t(1) << 30;  // 64-token tiles of all units
+  const int64_t most = int64_t(1) << 30;  // tiles of all units, in cost
+  // the tensor maps count a cache's tokens in 32 bits
+  if (a->prefix >= 2 * most || (a->batch > 0 && a->cap >= 2 * most / a->batch)) return false;
   if (a->prefix / 64 >= most || a->cap / 64 >= most || a->batch >= most / a->hq) return false;
   a->rows = a->batch * a->group;
   a->row_tiles = int((a->rows + 127) / 128);
   const int64_t pt = (a->prefix + a->tile - 1) / a->tile, tt = (a->cap + a->tile - 1) / a->tile;
   const int64_t punits = int64_t(a->hkv) * a->row_tiles, tunits = int64_t(a->hkv) * a->batch;
   if (tunits == 0) return true;  // no sequence: nothing runs
-  if (pt > most / punits || tt > most / tunits || punits * pt + tunits * tt >= most) return false;
+  if (pt > most / punits || tt > most / tunits || (punits * pt + tunits * tt) * 4 >= 2 * most) return false;
   a->ptiles = int(pt);
   a->grid = sm_count();
-  const int64_t ptotal = punits * pt;
-  int64_t per = (ptotal + a->grid - 1) / a->grid;  // a range is never shorter
-  if (per < kMinTiles) per = kMinTiles;
-  auto parts = [per](int64_t tiles) {
-    const int64_t p = tiles > 0 ? (tiles - 1) / per + 2 : 0;
+  // cost of a tile, measured: what fills it, plus the weights of more than 16 rows
+  a->pcost = a->d <= 128 && a->rows <= 16 ? 3 : 4;
+  a->tcost = a->d <= 128 && a->group <= 16 ? 3 : 4;
+  a->min_cost = kMinTiles * 4;
+  int64_t per = (punits * pt * a->pcost + a->grid - 1) / a->grid;  // a range is never shorter
+  if (per < a->min_cost) per = a->min_cost;
+  auto parts = [per](int64_t tiles, int cost) {
+    const int64_t p = tiles > 0 ? (tiles - 1) * cost / per + 2 : 0;
     return int(p < tiles ? p : tiles);
   };
-  a->parts_p = parts(pt);
-  a->parts_t = parts(tt);
+  a->parts_p = parts(pt, a->pcost);
+  a->parts_t = parts(tt, a->tcost);
   return true;
 }
 

@@ -14,6 +14,26 @@ __device__ __forceinline__ int shared_tail_len(const SharedArgs& a, int64_t b) {
   return int(n < 0 ? 0 : n > a.cap ? a.cap : n);
 }
 
+// Cost of the line's first `tile` tiles, the range that tile `tile` belongs to, and a
+// range's tiles [*pos, *end): those whose cost begins in it.
+__device__ __forceinline__ int64_t shared_cost(const SharedArgs& a, int tile) {
+  const int ptotal = a.hkv * a.row_tiles * a.ptiles;
+  return tile <= ptotal ? int64_t(tile) * a.pcost : int64_t(ptotal) * a.pcost + int64_t(tile - ptotal) * a.tcost;
+}
+__device__ __forceinline__ int range_of(const SharedArgs& a, int tile) {
+  return int(shared_cost(a, tile) / a.head[1]);
+}
+__device__ __forceinline__ void range_tiles(const SharedArgs& a, int range, int* pos, int* end) {
+  const int total = a.head[0], ptotal = a.hkv * a.row_tiles * a.ptiles;
+  auto tile_at = [&](int64_t cost) {
+    const int64_t p = int64_t(ptotal) * a.pcost;
+    const int64_t t = cost <= p ? (cost + a.pcost - 1) / a.pcost : ptotal + (cost - p + a.tcost - 1) / a.tcost;
+    return int(t < total ? t : total);
+  };
+  *pos = tile_at(int64_t(range) * a.head[1]);
+  *end = tile_at(int64_t(range + 1) * a.head[1]);
+}
+
 // A run of tiles of one unit inside one range.
 struct Segment {
   int part;            // 0: prefix, 1: tail
@@ -30,7 +50,6 @@ struct Segment {
 // The segment at position `pos` of the line (pos < end, the range's end).
 __device__ __forceinline__ Segment segment_at(const SharedArgs& a, int range, int pos, int end) {
   Segment s;
-  const int per = a.head[1];
   const int ptotal = a.hkv * a.row_tiles * a.ptiles;
   int first, at, unit_tiles;
   int64_t len;
@@ -69,7 +88,7 @@ __device__ __forceinline__ Segment segment_at(const SharedArgs& a, int range, in
   s.tiles = unit_tiles - at < end - pos ? unit_tiles - at : end - pos;
   s.t0 = int64_t(at) * a.tile;
   s.t1 = s.t0 + int64_t(s.tiles) * a.tile < len ? s.t0 + int64_t(s.tiles) * a.tile : len;
-  const int p = range - first / per + (s.part ? a.parts_p : 0);
+  const int p = range - range_of(a, first) + (s.part ? a.parts_p : 0);
   s.state = (int64_t(p) * a.hkv + s.g) * a.rows + s.row0;
   return s;
 }

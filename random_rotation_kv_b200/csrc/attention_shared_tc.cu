@@ -13,32 +13,46 @@
 // 2^15 and keep full precision down to 2^-22 of the largest.  The state (m', Σ 2^{x − m'}, O)
 // is what the merge takes.
 //
-// One CTA per SM walks its range of tiles (128 tokens, 64 for d = 256), 13 warps:
-//  * warps 4–11 read the packed codes one tile ahead into registers, turn code pairs into
-//    level pairs by one shared-memory lookup per byte (tables of 256 pairs, one copy per
-//    lane so that no bank conflicts; a value byte holds one coordinate of two tokens, so
-//    V is laid out transposed without a transposition) and write K [token][coordinate] and
-//    V [coordinate][token] as fp16 in the 128-byte swizzle, two stages each;
-//  * warp 12 issues the products: S from the queries in tensor memory and K, O from the
-//    weights in tensor memory and V; the next tile's S runs while this tile's weights
-//    are made;
-//  * warps 0–3 own one query row per thread: S from tensor memory, maximum, weights back
-//    into S's own columns as fp16, sums in registers.
+// Units of at most 16 rows (d ≤ 128) exchange the operands' roles: a tile's 128 tokens are the
+// rows of Sᵀ = C_K·Q'ᵀ and the coordinates the rows of Oᵀ = C_Vᵀ·Pᵀ, 16 columns wide, so that a
+// thread has a token's 8 rows to weigh instead of a row's 64 tokens of which most
+// rows would be empty.
+//
+// One CTA per SM walks its range of tiles (128 tokens, 64 for d = 256), 18 warps:
+//  * warp 17 copies the packed codes of two tiles ahead into shared memory (TMA boxes of
+//    half a tile's rows, swizzled where rows are 32, 64 or 128 bytes; rows of 8 and 24 bytes
+//    are not multiples of TMA's 16 and are read by the filling warps themselves);
+//  * warps 8–15 turn code pairs into level pairs by one shared-memory lookup per byte
+//    (tables of 256 pairs, one copy per lane so that no bank conflicts; a value byte holds
+//    one coordinate of two tokens, so V is laid out transposed without a transposition)
+//    and write K [token][coordinate] and V [coordinate][token] as fp16 in the 128-byte
+//    swizzle, V in two stages.  Row 8k + e of a tile's 64 is token 8k + (e + k) mod 8:
+//    the eight lanes that share a wavefront then read eight neighbouring code rows and
+//    write eight different chunks, for K and V alike;
+//  * warp 16 issues the products; the next tile's S runs while this tile's weights are made;
+//  * warps 0–7 make the weights: two threads per query row with half of the tokens each,
+//    the row's maximum met through shared memory, weights back into S's own columns as
+//    fp16 (or, for few rows, a thread per token and 8 rows, weights into shared memory).
 // Tensor memory: S twice, O and the queries (all of its 512 columns at d = 256).
 // Every wait is bounded; a wait that gives up makes the CTA's states NaN.
+#include <cstring>
+
 #include "attention_shared.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace rrq {
 namespace {
 
 constexpr uint32_t kWaitLimit = 1u << 24;  // polls, a few seconds in all
-constexpr int kSoftWarps = 4, kFillWarps = 8, kFill = kFillWarps * 32;
-constexpr int kThreads = (kSoftWarps + kFillWarps + 1) * 32;
+constexpr int kSoftWarps = 8, kFillWarps = 8, kFill = kFillWarps * 32;
+constexpr int kFewRows = 16;  // rows of a unit that exchanges the operands' roles
+constexpr int kThreads = (kSoftWarps + kFillWarps + 2) * 32;
 
 template <int D> struct Tc {
   static constexpr int TN = D <= 128 ? 128 : 64;     // tokens per tile
   static constexpr int OCT = D / 8 * TN / kFill;     // K octets per filling thread
+  static constexpr int PR = TN / 2;                  // rows of a piece of packed codes
   static constexpr uint32_t TILE = TN * D * 2;       // bytes of a K or V stage
   // shared addresses (the dynamic base is checked to be kBase)
   static constexpr uint32_t kBase = 0x400;
@@ -47,16 +61,23 @@ template <int D> struct Tc {
   static constexpr uint32_t FAIL = 0x4D0;
   static constexpr uint32_t VMAX = 0x500;            // [4 tiles][4 warps] largest value norm
   static constexpr uint32_t NK = 0x800, NV = 0x1000; // [4 tiles][TN] norms
-  static constexpr uint32_t K1 = 0x8000;             // K stage 1
+  static constexpr uint32_t PT = 0x2000;             // few rows: weights [2 tiles][2 × 64 tokens][16 rows], swizzled
+  static constexpr uint32_t QB = 0x4000;             // few rows: queries [part][64 coordinates][16 rows], swizzled
+  static constexpr uint32_t XCH = 0x6000;            // [2 tiles][2 halves][128 rows] maxima
+  // packed codes: eight 4 KB pieces of half a tile's rows, at most 64 (d = 256: 128) bytes each
+  static constexpr uint32_t piece(int stage, int v, int half) { return 0x8000u + uint32_t(stage * 4 + v * 2 + half) * 0x1000u; }
   static constexpr uint32_t TABLE = 0x10000;         // K pairs at +0, V pairs at +128 of every 256 bytes
-  static constexpr uint32_t K0 = 0x20000;
+  static constexpr uint32_t KT = 0x20000;            // K tile
   static constexpr uint32_t V0 = 0x28000;            // V stages
   static constexpr size_t kTotal = 0x38000 - kBase;
   // tensor memory columns
   static constexpr int S = 0, O = 2 * TN, Q = O + D, QL = Q + D / 2;
   static constexpr uint32_t idesc(int n) { return (1u << 4) | (uint32_t(n / 8) << 17) | ((128u / 16) << 24); }
-  static_assert(NV + 4 * TN * 4 <= 0x8000 && TILE <= 0x8000 && V0 + 2 * 0x8000 <= kBase + 227 * 1024, "layout");
+  static_assert(NV + 4 * TN * 4 <= PT && TILE <= 0x8000 && kTotal <= 227 * 1024, "layout");
 };
+
+// Token of row (column of S) n of a tile.
+__host__ __device__ constexpr int token_of(int n) { return (n & ~7) | ((n + (n >> 3)) & 7); }
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* fail) {
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
@@ -65,6 +86,12 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
   }
   *fail = 1;
   return false;
+}
+// True in one thread of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -89,6 +116,48 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+// AND of `v` over the `nthreads` threads (whole warps) meeting at named barrier `id`.
+__device__ __forceinline__ bool meet(uint32_t id, uint32_t nthreads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(v)), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// The power of two that stands for a tile's largest value norm.
+__device__ __forceinline__ float norm_unit(float big) {
+  return fminf(fmaxf(__uint_as_float(__float_as_uint(big) & 0x7f800000u), 0x1p-60f), 0x1p60f);
+}
+// m' of a running maximum m and the unit N: weights 2^{x − m'}·ν are at most 2^15.
+__device__ __forceinline__ float shifted(float m, float unit) {
+  return m - 8.f + float(int(__float_as_uint(unit) >> 23) - 127);
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
   float4 v;
@@ -99,26 +168,63 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// ---- the filling warps' reads and writes, by code width
-// Words of a K row that hold OCT octets, in loads as wide as their alignment allows.
-template <int B, int OCT> __device__ __forceinline__ void load_k(const uint8_t* p, uint32_t (&w)[8]) {
-  constexpr int W = OCT * B / 4;
+struct SharedMaps {
+  CUtensorMap k[2], v[2];  // prefix, tails
+};
+
+// Rows that TMA can move; the others are read from global memory by the filling warps.
+template <int D, int B> constexpr bool kBoxed = D * B / 8 % 16 == 0;
+
+// Byte `off` of row r in a piece of packed codes (the swizzle of head_rows_tensor_map).
+template <int PITCH> __device__ __forceinline__ uint32_t code_at(int r, uint32_t off) {
+  const uint32_t x = PITCH == 128 ? uint32_t(r) & 7u : PITCH == 64 ? uint32_t(r >> 1) & 3u : PITCH == 32 ? uint32_t(r >> 2) & 1u : 0u;
+  return uint32_t(r) * PITCH + (off ^ (x << 4));
+}
+__device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+// A shared word that later copies overwrite (lds_u32 is for constant tables).
+__device__ __forceinline__ uint32_t lds_code(uint32_t addr, int bytes) {
+  uint32_t v;
+  if (bytes == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  else if (bytes == 2) asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(addr));
+  else asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// ---- the filling warps' reads, by code width
+// OCT octets from byte sub·OCT·B of a K row: from a piece (row r), or from global memory.
+template <int D, int B, int OCT>
+__device__ __forceinline__ void read_k(uint32_t piece, int r, int sub, uint32_t (&w)[8]) {
+  constexpr int W = OCT * B / 4, PITCH = D * B / 8;
+  const uint32_t off = uint32_t(sub) * (OCT * B);
   if constexpr (W % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = lds_u4(piece + code_at<PITCH>(r, off + 4 * i));
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
     }
   } else if constexpr (W % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
-      w[2 * i] = v.x, w[2 * i + 1] = v.y;
+    for (int i = 0; i < W; i += 2) {
+      const uint2 v = lds_u2(piece + code_at<PITCH>(r, off + 4 * i));
+      w[i] = v.x, w[i + 1] = v.y;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    for (int i = 0; i < W; ++i) w[i] = lds_code(piece + code_at<PITCH>(r, off + 4 * i), 4);
   }
+}
+template <int B, int OCT> __device__ __forceinline__ void fetch_k(const uint8_t* p, uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < OCT * B / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
 }
 // Octet i of those words as nibbles.
 template <int B> __device__ __forceinline__ uint32_t octet_of(const uint32_t (&w)[8], int i) {
@@ -128,18 +234,28 @@ template <int B> __device__ __forceinline__ uint32_t octet_of(const uint32_t (&w
   if (sh + 8 * B > 32) v = __funnelshift_r(w[k], w[k + 1 < 8 ? k + 1 : 7], sh);
   return octet_nibbles(v & (B == 3 ? 0xffffffu : B == 2 ? 0xffffu : 0xffu), B);
 }
-// The B bytes of octet o of 8 rows (3-bit octets as the two words they may touch).
-template <int B>
-__device__ __forceinline__ void load_v(const uint8_t* const (&p)[8], int o, uint32_t (&w)[16]) {
+// The B bytes of octet o of the 8 tokens of block kb, token 8·kb + (r + kb) mod 8 in w[r]
+// (3-bit octets as the two words they may touch).
+template <int D, int B>
+__device__ __forceinline__ void read_v(uint32_t piece, int row0, int kb, int o, uint32_t (&w)[16]) {
+  constexpr int PITCH = D * B / 8;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    if constexpr (B == 4) w[r] = __ldg(reinterpret_cast<const uint32_t*>(p[r]) + o);
-    else if constexpr (B == 2) w[r] = __ldg(reinterpret_cast<const uint16_t*>(p[r]) + o);
-    else if constexpr (B == 1) w[r] = __ldg(p[r] + o);
-    else {
-      w[r] = __ldg(reinterpret_cast<const uint32_t*>(p[r]) + (3 * o) / 4);
-      w[8 + r] = __ldg(reinterpret_cast<const uint32_t*>(p[r]) + (3 * o + 2) / 4);
+    const int row = row0 + ((r + kb) & 7);
+    if constexpr (B == 3) {
+      w[r] = lds_code(piece + code_at<PITCH>(row, uint32_t((3 * o) / 4 * 4)), 4);
+      w[8 + r] = lds_code(piece + code_at<PITCH>(row, uint32_t((3 * o + 2) / 4 * 4)), 4);
+    } else {
+      w[r] = lds_code(piece + code_at<PITCH>(row, uint32_t(o * B)), B);
     }
+  }
+}
+template <int B> __device__ __forceinline__ void fetch_v(const uint8_t* p, int r, int o, uint32_t (&w)[16]) {
+  if constexpr (B == 3) {
+    w[r] = __ldg(reinterpret_cast<const uint32_t*>(p) + (3 * o) / 4);
+    w[8 + r] = __ldg(reinterpret_cast<const uint32_t*>(p) + (3 * o + 2) / 4);
+  } else {
+    w[r] = __ldg(p + o);  // one-bit octets
   }
 }
 
@@ -187,15 +303,22 @@ __device__ __forceinline__ void put_v(const uint32_t (&w)[16], int o, uint32_t r
   put(7, std::integral_constant<int, 3>{}, od);
 }
 
+// Columns [h, h + 32) of a tile: `v` where the column's token is not one of the first `valid`.
+__device__ __forceinline__ void mask(float2 (&y)[16], int h, int valid, float v) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int n = h + 2 * k;
+    if (token_of(n) >= valid) y[k].x = v;
+    if (token_of(n + 1) >= valid) y[k].y = v;
+  }
+}
+
 // Position in a range, one tile at a time.
 struct Cursor {
   int range, pos, end, i;
   Segment s;
   __device__ __forceinline__ Cursor(const SharedArgs& a, int r) : range(r), i(0) {
-    const int64_t start = int64_t(r) * a.head[1];
-    const int total = a.head[0];
-    pos = int(start < total ? start : total);
-    end = int(start + a.head[1] < total ? start + a.head[1] : total);
+    range_tiles(a, r, &pos, &end);
     if (pos < end) s = segment_at(a, range, pos, end);
   }
   __device__ __forceinline__ bool live() const { return pos < end; }
@@ -209,7 +332,7 @@ struct Cursor {
 };
 
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ SharedMaps maps) {
   using L = Tc<D>;
   constexpr int TN = L::TN;
   extern __shared__ __align__(1024) uint8_t dsm[];
@@ -224,6 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   auto s_full = [&](int j) { return &bars[5 + (j & 1)]; };
   auto p_full = [&](int j) { return &bars[7 + (j & 1)]; };
   auto o_done = [&](int j) { return &bars[9 + (j & 1)]; };
+  auto c_full = [&](int j) { return &bars[12 + (j & 1)]; };
+  auto c_free = [&](int j) { return &bars[14 + (j & 1)]; };
   auto phase = [](int j) { return uint32_t(j >> 1) & 1u; };
   uint32_t* tslot = reinterpret_cast<uint32_t*>(at(L::TSLOT));
   volatile int* fail = reinterpret_cast<volatile int*>(at(L::FAIL));
@@ -237,6 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), kSoftWarps);
       mbar_init(o_done(s), 1);
+      mbar_init(c_full(s), 1);
+      mbar_init(c_free(s), kFillWarps);
     }
     *fail = placed ? 0 : 1;
     fence_mbarrier_init();
@@ -261,173 +388,325 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   pdl_wait();  // from here on, global memory
 
   if (warp < kSoftWarps) {
-    // ---------------------------------------------------------------- softmax: thread = query row
-    const uint32_t tl = tmem + (uint32_t(32 * warp) << 16);
+    // ---------------------------------------------------------------- weights
+    const int quarter = warp & 3, half = warp >> 2;  // tensor-memory lanes, half of the tokens (of the rows)
+    const int ln = 32 * quarter + lane;              // this thread's tensor-memory lane
+    const uint32_t tl = tmem + (uint32_t(32 * quarter) << 16);
     Cursor c(a, range);
     int j = 0;
     while (c.live()) {
       const Segment& s = c.s;
-      const bool row_ok = tid < s.nrows, warp_ok = 32 * warp < s.nrows;
-      const int64_t qrow = int64_t(s.g) * a.rows + s.row0 + (row_ok ? tid : 0);
       bool ok = *fail == 0;
-      float rs = 1.f;
-      if (warp_ok) {
-        rs = a.qexp[qrow];
+      if (D <= 128 && s.nrows <= kFewRows) {
+        if constexpr (D <= 128) {
+          // ---- few rows: lane = token, columns = rows; this half's rows [8·half, + 8)
+          const int64_t qrow = int64_t(s.g) * a.rows + s.row0;
+          {
+            const int r = (tid >> 3) & 15, k0 = (tid & 7) + ((tid >> 7) << 3);  // row, chunk of 8 coordinates
 #pragma unroll
-        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-          const uint4* q = reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + qrow * D);
+            for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+              if (k0 < D / 8) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < s.nrows) v = __ldcg(reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + (qrow + r) * D) + k0);
+                sts_v4(L::QB + uint32_t(part * (D / 64) + (k0 >> 3)) * 2048 + uint32_t(r) * 128 + (uint32_t((k0 ^ r) & 7) << 4),
+                       v.x, v.y, v.z, v.w);
+              }
+          }
+          fence_proxy_async_smem();
+          const bool mine = 8 * half < s.nrows;
+          float rs[8], m[8], mp[8], l[8];
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t r[16];
+          for (int r = 0; r < 8; ++r) {
+            rs[r] = 8 * half + r < s.nrows ? a.qexp[qrow + 8 * half + r] : 1.f;
+            m[r] = mp[r] = l[r] = 0.f;
+          }
+          float vn = 0.f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+          for (int i = 0; i < s.tiles; ++i, ++j) {
+            ok = ok && wait_for(s_full(j), phase(j), fail);
+            ok = __all_sync(kFull, ok);
+            tc_fence_after();
+            if (mine) {
+              const int64_t left = s.t1 - s.t0 - int64_t(i) * TN;
+              const bool live = token_of(ln) < left;
+              const uint32_t wm = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(half) * 128;
+              float y[8], nv = 0.f;
+              if (ok) {
+                uint32_t v[8];
+                tmem_ld8(tl + uint32_t(L::S + (j & 1) * TN + 8 * half), v);
+                const float nk = __uint_as_float(lds_code(L::NK + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4, 4));
+                nv = __uint_as_float(lds_code(L::NV + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4, 4));
+                tmem_ld_wait();
+                float mx[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 v = __ldcg(q + 4 * i + k);
-              r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
+                for (int r = 0; r < 8; ++r) {
+                  y[r] = live ? __uint_as_float(v[r]) * nk : -INFINITY;
+                  mx[r] = warp_max(y[r]);
+                }
+                if (lane < 2)
+                  sts_v4(wm + uint32_t(quarter) * 32 + uint32_t(lane) * 16, __float_as_uint(lane ? mx[4] : mx[0]),
+                         __float_as_uint(lane ? mx[5] : mx[1]), __float_as_uint(lane ? mx[6] : mx[2]),
+                         __float_as_uint(lane ? mx[7] : mx[3]));
+              }
+              ok = meet(uint32_t(5 + half), 128, ok);
+              if (ok) {
+                float mx[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float4 x0 = lds_f4(wm + uint32_t(q) * 32), x1 = lds_f4(wm + uint32_t(q) * 32 + 16);
+                  const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                  for (int r = 0; r < 8; ++r) mx[r] = q ? fmaxf(mx[r], x[r]) : x[r];
+                }
+                const float4 vm = lds_f4(L::VMAX + uint32_t(j & 3) * 16);
+                const float pw = norm_unit(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)));
+                if (i == 0) {
+                  vn = pw;
+#pragma unroll
+                  for (int r = 0; r < 8; ++r) {
+                    m[r] = mx[r] * rs[r];
+                    mp[r] = shifted(m[r], vn);
+                  }
+                } else {
+                  const bool wide = pw > 4.f * vn;
+                  bool up = wide;
+#pragma unroll
+                  for (int r = 0; r < 8; ++r) up = up || mx[r] * rs[r] > m[r] + 4.f;
+                  if (up) {  // the same in every thread of the half
+                    if (wide) vn = pw;
+                    ok = __all_sync(kFull, wait_for(o_done(j - 1), phase(j - 1), fail));
+                    tc_fence_after();
+                    uint32_t o[8];
+                    tmem_ld8(tl + uint32_t(L::O + 8 * half), o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                      if (mx[r] * rs[r] > m[r] + 4.f) m[r] = mx[r] * rs[r];
+                      const float mn = shifted(m[r], vn), f = ex2(mp[r] - mn);
+                      mp[r] = mn;
+                      l[r] *= f;
+                      o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
+                    }
+                    tmem_st8(tl + uint32_t(L::O + 8 * half), o);
+                    tmem_st_wait();
+                  }
+                }
+                const uint32_t pt = L::PT + uint32_t(j & 1) * 4096 + uint32_t(ln >> 6) * 2048 + uint32_t(ln & 7) * 2;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                  const float p = live ? ex2(fmaf(y[r], rs[r], -mp[r])) : 0.f;
+                  l[r] += p;
+                  const __half w = __float2half_rn(p * nv);
+                  asm volatile("st.shared.b16 [%0], %1;" ::"r"(pt + uint32_t(8 * half + r) * 128 + (uint32_t(((ln >> 3) ^ r) & 7) << 4)),
+                               "h"(*reinterpret_cast<const unsigned short*>(&w))
+                               : "memory");
+                }
+                fence_proxy_async_smem();
+              }
             }
-            tmem_st16(tl + uint32_t((part ? L::QL : L::Q) + 16 * i), r);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(j));
+          }
+          ok = ok && wait_for(o_done(j - 1), phase(j - 1), fail);
+          ok = __all_sync(kFull, ok);
+          tc_fence_after();
+          if (mine) {
+            // the half's sums over its tokens, four warps through shared memory
+            const uint32_t wl = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(half) * 128;
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(kFull, l[r], o);
+            if (lane == 0) {
+              sts_v4(wl + uint32_t(quarter) * 32, __float_as_uint(l[0]), __float_as_uint(l[1]), __float_as_uint(l[2]), __float_as_uint(l[3]));
+              sts_v4(wl + uint32_t(quarter) * 32 + 16, __float_as_uint(l[4]), __float_as_uint(l[5]), __float_as_uint(l[6]), __float_as_uint(l[7]));
+            }
+            ok = meet(uint32_t(5 + half), 128, ok);
+            if (quarter == 0 && lane < 8 && 8 * half + lane < s.nrows) {
+              float sum = 0.f, mine_mp = mp[0];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) sum += __uint_as_float(lds_code(wl + uint32_t(q) * 32 + uint32_t(lane) * 4, 4));
+#pragma unroll
+              for (int r = 1; r < 8; ++r)
+                if (lane == r) mine_mp = mp[r];
+              a.stats[s.state + 8 * half + lane] = ok ? make_float2(mine_mp, sum) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
+            }
+            if (ok) {
+              uint32_t o[8];
+              tmem_ld8(tl + uint32_t(L::O + 8 * half), o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int r = 0; r < 8; ++r)
+                if (8 * half + r < s.nrows && ln < D) a.acc[(s.state + 8 * half + r) * D + ln] = __uint_as_float(o[r]);
+            }
+            // the next segment writes this slot of the exchange again
+            meet(uint32_t(5 + half), 128, true);
           }
         }
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-
-      float m = 0.f, mp = 0.f, vn = 0.f;  // running maximum, m', N
-      float2 l2 = make_float2(0.f, 0.f);
-      for (int i = 0; i < s.tiles; ++i, ++j) {
-        ok = ok && wait_for(s_full(j), phase(j), fail);
-        ok = __all_sync(kFull, ok);
-        tc_fence_after();
-        if (warp_ok && ok) {
-          const int64_t left = s.t1 - s.t0 - int64_t(i) * TN;
-          const int valid = int(left < TN ? left : TN);
-          const uint32_t sb = tl + uint32_t(L::S + (j & 1) * TN);
-          const uint32_t nk = L::NK + uint32_t(j & 3) * (TN * 4), nv = L::NV + uint32_t(j & 3) * (TN * 4);
-          // the largest ν^K·S of the row
-          float mx = -INFINITY;
+      } else {
+        // ---- lane = query row; this half's tokens [half·TN/2, + TN/2)
+        constexpr int TH = TN / 2, DH = D / 2;
+        const bool row_ok = ln < s.nrows, warp_ok = 32 * quarter < s.nrows;
+        const int64_t qrow = int64_t(s.g) * a.rows + s.row0 + (row_ok ? ln : 0);
+        float rs = 1.f;
+        if (warp_ok) {
+          rs = a.qexp[qrow];
 #pragma unroll
-          for (int h = 0; h < TN / 64; ++h) {
-            uint32_t v[2][32];
-            tmem_ld32(sb + 64 * h, v[0]);
-            tmem_ld32(sb + 64 * h + 32, v[1]);
-            tmem_ld_wait();
-            auto fold = [&](auto full) {
-#pragma unroll
-              for (int k = 0; k < 64; k += 4) {
-                const float4 n = lds_f4(nk + uint32_t(64 * h + k) * 4);
-                const uint32_t* x = &v[k >> 5][k & 31];
-                const float2 y0 = mul2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(n.x, n.y));
-                const float2 y1 = mul2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(n.z, n.w));
-                if constexpr (decltype(full)::value) {
-                  mx = fmaxf(fmaxf(mx, fmaxf(y0.x, y0.y)), fmaxf(y1.x, y1.y));
-                } else {
-                  const int t = 64 * h + k;
-                  if (t < valid) mx = fmaxf(mx, y0.x);
-                  if (t + 1 < valid) mx = fmaxf(mx, y0.y);
-                  if (t + 2 < valid) mx = fmaxf(mx, y1.x);
-                  if (t + 3 < valid) mx = fmaxf(mx, y1.y);
-                }
-              }
-            };
-            if (valid == TN) fold(std::true_type{});
-            else fold(std::false_type{});
-          }
-          mx *= rs;
-          const float4 vm = lds_f4(L::VMAX + uint32_t(j & 3) * 16);
-          const float big = TN == 128 ? fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)) : fmaxf(vm.x, vm.y);
-          const float pw = fminf(fmaxf(__uint_as_float(__float_as_uint(big) & 0x7f800000u), 0x1p-60f), 0x1p60f);
-          if (i == 0) {
-            m = mx;
-            vn = pw;
-            mp = m - 8.f + float(int(__float_as_uint(vn) >> 23) - 127);
-          } else {
-            const bool up = mx > m + 4.f, wide = pw > 4.f * vn;
-            if (__any_sync(kFull, up || wide)) {
-              if (up) m = mx;
-              if (wide) vn = pw;
-              const float mn = m - 8.f + float(int(__float_as_uint(vn) >> 23) - 127);
-              const float f = ex2(mp - mn);
-              mp = mn;
-              l2 = mul2(l2, make_float2(f, f));
-              ok = __all_sync(kFull, wait_for(o_done(j - 1), phase(j - 1), fail));
-              tc_fence_after();
-              if (ok) {
+          for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+            const uint4* q = reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + qrow * D + half * DH);
 #pragma unroll 1
-                for (int k = 0; k < D; k += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(tl + uint32_t(L::O + k), o);
-                  tmem_ld_wait();
+            for (int i = 0; i < DH / 32; ++i) {
+              uint32_t r[16];
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st16(tl + uint32_t(L::O + k), o);
-                }
-                tmem_st_wait();
+              for (int k = 0; k < 4; ++k) {
+                const uint4 v = __ldcg(q + 4 * i + k);
+                r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
               }
+              tmem_st16(tl + uint32_t((part ? L::QL : L::Q) + half * (DH / 2) + 16 * i), r);
             }
-          }
-          // weights into S's columns, the sum of the exponentials
-          const float2 rs2 = make_float2(rs, rs), mp2 = make_float2(-mp, -mp);
-#pragma unroll
-          for (int h = 0; h < TN / 32; ++h) {
-            uint32_t v[32], p[16];
-            tmem_ld32(sb + 32 * h, v);
-            tmem_ld_wait();
-            auto weigh = [&](auto full) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const float4 n = lds_f4(nk + uint32_t(32 * h + k) * 4), w = lds_f4(nv + uint32_t(32 * h + k) * 4);
-                const float2 x0 = fma2(mul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), make_float2(n.x, n.y)), rs2, mp2);
-                const float2 x1 = fma2(mul2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), make_float2(n.z, n.w)), rs2, mp2);
-                float2 e0 = make_float2(ex2(x0.x), ex2(x0.y)), e1 = make_float2(ex2(x1.x), ex2(x1.y));
-                if constexpr (!decltype(full)::value) {
-                  const int t = 32 * h + k;
-                  if (t >= valid) e0.x = 0.f;
-                  if (t + 1 >= valid) e0.y = 0.f;
-                  if (t + 2 >= valid) e1.x = 0.f;
-                  if (t + 3 >= valid) e1.y = 0.f;
-                }
-                l2 = add2(l2, e0);
-                l2 = add2(l2, e1);
-                const float2 w0 = mul2(e0, make_float2(w.x, w.y)), w1 = mul2(e1, make_float2(w.z, w.w));
-                const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
-                p[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-                p[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-              }
-            };
-            if (valid == TN) weigh(std::true_type{});
-            else weigh(std::false_type{});
-            tmem_st16(sb + 16 * h, p);
           }
           tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(j));
-      }
-      // the segment's state
-      ok = ok && wait_for(o_done(j - 1), phase(j - 1), fail);
-      ok = __all_sync(kFull, ok);
-      tc_fence_after();
-      if (warp_ok) {
-        const int64_t st = s.state + tid;
-        if (row_ok)
-          a.stats[st] = ok ? make_float2(mp, l2.x + l2.y) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
-        if (ok) {
+        if (lane == 0) mbar_arrive(q_full);
+
+        float m = 0.f, mp = 0.f, vn = 0.f;  // running maximum, m', N
+        float2 l2 = make_float2(0.f, 0.f), l3 = l2;
+        const uint32_t pair = uint32_t(1 + quarter);
+        for (int i = 0; i < s.tiles; ++i, ++j) {
+          ok = ok && wait_for(s_full(j), phase(j), fail);
+          ok = __all_sync(kFull, ok);
+          tc_fence_after();
+          if (warp_ok) {
+            const int64_t left = s.t1 - s.t0 - int64_t(i) * TN;
+            const int valid = int(left < TN ? left : TN);
+            const bool full = valid == TN;
+            const uint32_t sb = tl + uint32_t(L::S + (j & 1) * TN + half * TH);
+            const uint32_t nk = L::NK + uint32_t((j & 3) * TN + half * TH) * 4, nv = L::NV + uint32_t((j & 3) * TN + half * TH) * 4;
+            const uint32_t xch = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(ln) * 4;
+            float mx = -INFINITY;
+            if (ok) {
+              // the largest ν^K·S of the row's half (loops kept rolled: unrolled, the warps'
+              // different code ran out of the instruction cache)
 #pragma unroll 1
-          for (int k = 0; k < D; k += 32) {
-            uint32_t o[32];
-            tmem_ld32(tl + uint32_t(L::O + k), o);
-            tmem_ld_wait();
-            if (row_ok) {
-              float* dst = a.acc + st * D + k;
+              for (int h = 0; h < TH; h += 32) {
+                uint32_t v[32];
+                tmem_ld32(sb + h, v);
+                tmem_ld_wait();
+                float2 y[16];
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + e), "r"(o[e]), "r"(o[e + 1]),
-                             "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7])
-                             : "memory");
+                for (int k = 0; k < 32; k += 4) {
+                  const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
+                  y[k / 2] = mul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), make_float2(n.x, n.y));
+                  y[k / 2 + 1] = mul2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), make_float2(n.z, n.w));
+                }
+                if (!full) mask(y, half * TH + h, valid, -INFINITY);
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) mx = fmaxf(mx, fmaxf(fmaxf(y[k].x, y[k].y), fmaxf(y[k + 1].x, y[k + 1].y)));
+              }
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + uint32_t(half) * 512), "f"(mx) : "memory");
+            }
+            ok = meet(pair, 64, ok);
+            if (ok) {
+              mx = fmaxf(mx, __uint_as_float(lds_code(xch + uint32_t(half ^ 1) * 512, 4))) * rs;
+              const float4 vm = lds_f4(L::VMAX + uint32_t(j & 3) * 16);
+              const float pw = norm_unit(TN == 128 ? fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)) : fmaxf(vm.x, vm.y));
+              if (i == 0) {
+                m = mx;
+                vn = pw;
+                mp = shifted(m, vn);
+              } else {
+                const bool up = mx > m + 4.f, wide = pw > 4.f * vn;
+                if (__any_sync(kFull, up || wide)) {
+                  if (up) m = mx;
+                  if (wide) vn = pw;
+                  const float mn = shifted(m, vn), f = ex2(mp - mn);
+                  mp = mn;
+                  l2 = mul2(l2, make_float2(f, f));
+                  l3 = mul2(l3, make_float2(f, f));
+                  ok = __all_sync(kFull, wait_for(o_done(j - 1), phase(j - 1), fail));
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int k = 0; k < DH; k += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tl + uint32_t(L::O + half * DH + k), o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st32(tl + uint32_t(L::O + half * DH + k), o);
+                  }
+                  tmem_st_wait();
+                }
+              }
+              // weights into S's columns, the sum of the exponentials
+              const float2 rs2 = make_float2(rs, rs), mp2 = make_float2(-mp, -mp);
+              const uint32_t pb = sb;  // the first half of the columns that this thread reads
+#pragma unroll 1
+              for (int h = 0; h < TH; h += 32) {
+                uint32_t v[32], p[16];
+                tmem_ld32(sb + h, v);
+                tmem_ld_wait();
+                float2 e[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                  const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
+                  const float2 x0 = fma2(mul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), make_float2(n.x, n.y)), rs2, mp2);
+                  const float2 x1 = fma2(mul2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), make_float2(n.z, n.w)), rs2, mp2);
+                  e[k / 2] = make_float2(ex2(x0.x), ex2(x0.y));
+                  e[k / 2 + 1] = make_float2(ex2(x1.x), ex2(x1.y));
+                }
+                if (!full) mask(e, half * TH + h, valid, 0.f);
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                  const float4 w = lds_f4(nv + uint32_t(h + k) * 4);
+                  l2 = add2(l2, e[k / 2]);
+                  l3 = add2(l3, e[k / 2 + 1]);
+                  const float2 w0 = mul2(e[k / 2], make_float2(w.x, w.y)), w1 = mul2(e[k / 2 + 1], make_float2(w.z, w.w));
+                  const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
+                  p[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+                  p[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                }
+                tmem_st16(pb + h / 2, p);
+              }
+              tmem_st_wait();
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(j));
+        }
+        // the segment's state
+        ok = ok && wait_for(o_done(j - 1), phase(j - 1), fail);
+        ok = __all_sync(kFull, ok);
+        tc_fence_after();
+        if (warp_ok) {
+          const uint32_t xch = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(ln) * 4;
+          const float sum = (l2.x + l2.y) + (l3.x + l3.y);
+          if (half) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch), "f"(sum) : "memory");
+          ok = meet(pair, 64, ok);
+          const int64_t st = s.state + ln;
+          if (!half && row_ok)
+            a.stats[st] = ok ? make_float2(mp, sum + __uint_as_float(lds_code(xch, 4))) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
+          if (ok) {
+#pragma unroll 1
+            for (int k = 0; k < DH; k += 32) {
+              uint32_t o[32];
+              tmem_ld32(tl + uint32_t(L::O + half * DH + k), o);
+              tmem_ld_wait();
+              if (row_ok) {
+                float* dst = a.acc + st * D + half * DH + k;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + e), "r"(o[e]), "r"(o[e + 1]),
+                               "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7])
+                               : "memory");
+              }
+            }
+          }
+          meet(pair, 64, true);  // the next segment writes this slot of the exchange again
         }
       }
       c.i = s.tiles - 1;
@@ -436,139 +715,185 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   } else if (warp < kSoftWarps + kFillWarps) {
     // ------------------------------------------------------------ codes to fp16 levels in shared memory
     const int ft = tid - kSoftWarps * 32;
-    const int tok = ft % TN, sub = ft / TN;               // K: one token, OCT octets from sub·OCT
+    const int n = ft % TN, sub = ft / TN;                 // K: row n, OCT octets from sub·OCT
+    const int tok = token_of(n);                          // its token
     const int c0 = (sub * L::OCT) & 7, kblock = sub * L::OCT / 8;
     const int kb = lane & 7, rest = ft >> 3;              // V: 8 tokens, one octet
     const int vo = rest % (D / 8), vblock = rest / (D / 8);
     const bool v_mine = vblock < TN / 64;
+    const int v_tok = 64 * vblock + 8 * kb;
     const uint32_t kword = L::TABLE | uint32_t(lane * 4), vword = kword | 128u;
-    const uint32_t krow = uint32_t(kblock) * (TN * 128) + uint32_t(tok) * 128;
+    const uint32_t krow = uint32_t(kblock) * (TN * 128) + uint32_t(n) * 128;
     const uint32_t vrow = uint32_t(vblock) * (D * 128) + uint32_t(8 * vo) * 128;
     uint32_t kw[8], vw[16];
     float norm_k = 0.f, norm_v = 0.f;
-    auto fetch_k = [&](const Cursor& c) {
+    // what comes from global memory for the cursor's tile: norms, and rows no box can move
+    auto fetch = [&](const Cursor& c) {
       const Segment& s = c.s;
-      const int64_t t = s.t0 + int64_t(c.i) * TN + tok;
-      const int64_t row = (s.token_base + (t < s.t1 ? t : s.t1 - 1)) * a.hkv + s.g;
-      const uint8_t* base = a.k_codes[s.part] + row * (D * a.k_bits / 8) + sub * L::OCT * a.k_bits;
-      switch (a.k_bits) {
-        case 1: load_k<1, L::OCT>(base, kw); break;
-        case 2: load_k<2, L::OCT>(base, kw); break;
-        case 3: load_k<3, L::OCT>(base, kw); break;
-        default: load_k<4, L::OCT>(base, kw); break;
-      }
+      auto row_of = [&](int t) {
+        const int64_t tt = s.t0 + int64_t(c.i) * TN + t;
+        return (s.token_base + (tt < s.t1 ? tt : s.t1 - 1)) * a.hkv + s.g;
+      };
+      const int64_t row = row_of(tok);
       if (sub == 0) {
         norm_k = __ldg(a.k_norms[s.part] + row);
-        norm_v = t < s.t1 ? __ldg(a.v_norms[s.part] + row) : 0.f;
+        norm_v = s.t0 + int64_t(c.i) * TN + tok < s.t1 ? __ldg(a.v_norms[s.part] + row) : 0.f;
+      }
+      if constexpr (D == 64) {
+        const uint8_t* kc = a.k_codes[s.part] + row * (D * a.k_bits / 8) + sub * L::OCT * a.k_bits;
+        if (a.k_bits == 1) fetch_k<1, L::OCT>(kc, kw);
+        else if (a.k_bits == 3) fetch_k<3, L::OCT>(kc, kw);
+        if (v_mine && (a.v_bits & 1)) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const uint8_t* vc = a.v_codes[s.part] + row_of(v_tok + ((r + kb) & 7)) * (D * a.v_bits / 8);
+            if (a.v_bits == 1) fetch_v<1>(vc, r, vo, vw);
+            else fetch_v<3>(vc, r, vo, vw);
+          }
+        }
       }
     };
-    auto fetch_v = [&](const Cursor& c) {
-      if (!v_mine) return;
-      const Segment& s = c.s;
-      const uint8_t* p[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int64_t t = s.t0 + int64_t(c.i) * TN + 64 * vblock + 8 * kb + r;
-        p[r] = a.v_codes[s.part] + ((s.token_base + (t < s.t1 ? t : s.t1 - 1)) * a.hkv + s.g) * (D * a.v_bits / 8);
-      }
-      switch (a.v_bits) {
-        case 1: load_v<1>(p, vo, vw); break;
-        case 2: load_v<2>(p, vo, vw); break;
-        case 3: load_v<3>(p, vo, vw); break;
-        default: load_v<4>(p, vo, vw); break;
-      }
+    auto fill_k = [&](auto bits, int j) {
+      constexpr int B = decltype(bits)::value;
+      if constexpr (kBoxed<D, B>) read_k<D, B, L::OCT>(L::piece(j & 1, 0, tok / L::PR), tok % L::PR, sub, kw);
+      put_k<B, L::OCT>(kw, L::KT + krow, c0, n, kword);
+    };
+    auto fill_v = [&](auto bits, int j) {
+      constexpr int B = decltype(bits)::value;
+      if constexpr (kBoxed<D, B>) read_v<D, B>(L::piece(j & 1, 1, v_tok / L::PR), v_tok % L::PR, kb, vo, vw);
+      put_v<B>(vw, vo, L::V0 + uint32_t(j & 1) * 0x8000u + vrow, kb, vword);
     };
     Cursor c(a, range);
-    if (c.live()) {
-      fetch_k(c);
-      fetch_v(c);
-    }
+    if (c.live()) fetch(c);
     bool ok = placed;
     for (int j = 0; c.live(); ++j) {
-      Cursor n = c;
-      n.next(a);
-      if (j >= 2) ok = ok && wait_for(s_full(j), phase(j - 2), fail);
+      ok = ok && wait_for(c_full(j), phase(j), fail);
+      if (j >= 1) ok = ok && wait_for(s_full(j - 1), phase(j - 1), fail);
       ok = __all_sync(kFull, ok);
       if (!ok) break;
+      // the slot's last reader was tile j − 4: its weights were made before S of tile j − 1 began
       if (sub == 0) {
-        const uint32_t slot = uint32_t(j & 3) * (TN * 4) + uint32_t(tok) * 4;
+        const uint32_t slot = uint32_t(j & 3) * (TN * 4) + uint32_t(n) * 4;
         *reinterpret_cast<float*>(at(L::NK + slot)) = norm_k;
         *reinterpret_cast<float*>(at(L::NV + slot)) = norm_v;
         float big = norm_v;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-        if (lane == 0) *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(tok >> 5) * 4)) = big;
+        if (lane == 0) *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = big;
       }
-      {
-        const uint32_t row = (j & 1 ? L::K1 : L::K0) + krow;
-        switch (a.k_bits) {
-          case 1: put_k<1, L::OCT>(kw, row, c0, tok, kword); break;
-          case 2: put_k<2, L::OCT>(kw, row, c0, tok, kword); break;
-          case 3: put_k<3, L::OCT>(kw, row, c0, tok, kword); break;
-          default: put_k<4, L::OCT>(kw, row, c0, tok, kword); break;
-        }
+      switch (a.k_bits) {
+        case 1: fill_k(std::integral_constant<int, 1>{}, j); break;
+        case 2: fill_k(std::integral_constant<int, 2>{}, j); break;
+        case 3: fill_k(std::integral_constant<int, 3>{}, j); break;
+        default: fill_k(std::integral_constant<int, 4>{}, j); break;
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full(j));
-      if (n.live()) fetch_k(n);
       if (j >= 2) ok = wait_for(o_done(j), phase(j - 2), fail);
       ok = __all_sync(kFull, ok);
       if (!ok) break;
       if (v_mine) {
-        const uint32_t row = L::V0 + uint32_t(j & 1) * 0x8000u + vrow;
         switch (a.v_bits) {
-          case 1: put_v<1>(vw, vo, row, kb, vword); break;
-          case 2: put_v<2>(vw, vo, row, kb, vword); break;
-          case 3: put_v<3>(vw, vo, row, kb, vword); break;
-          default: put_v<4>(vw, vo, row, kb, vword); break;
+          case 1: fill_v(std::integral_constant<int, 1>{}, j); break;
+          case 2: fill_v(std::integral_constant<int, 2>{}, j); break;
+          case 3: fill_v(std::integral_constant<int, 3>{}, j); break;
+          default: fill_v(std::integral_constant<int, 4>{}, j); break;
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(v_full(j));
-      if (n.live()) fetch_v(n);
-      c = n;
+      if (lane == 0) {
+        mbar_arrive(v_full(j));
+        mbar_arrive(c_free(j));
+      }
+      c.next(a);
+      if (c.live()) fetch(c);
     }
-  } else if (lane == 0) {
-    // ---------------------------------------------------------------- one thread issues the products
+  } else if (warp == kSoftWarps + kFillWarps + 1) {
+    // ---------------------------------------------------------------- one thread copies the packed codes
+    if (lane == 0) {
+      const bool kbox = D * a.k_bits / 8 % 16 == 0, vbox = D * a.v_bits / 8 % 16 == 0;
+      const int krow = D * a.k_bits / 8, vrow = D * a.v_bits / 8;
+      const uint32_t bytes = (kbox ? TN * krow : 0) + (vbox ? TN * vrow : 0);
+      bool ok = placed;
+      int j = 0;
+      for (Cursor c(a, range); c.live(); c.next(a), ++j) {
+        if (j >= 2) ok = ok && wait_for(c_free(j), phase(j - 2), fail);
+        if (!ok) break;
+        const uint32_t bar = smem_addr(c_full(j));
+        mbarrier_expect_tx(bar, bytes);
+        const int64_t t = c.s.token_base + c.s.t0 + int64_t(c.i) * TN;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t y = t + h * L::PR;  // rows past the cache's end are filled with zeros
+          if (kbox) tma_load_2d(L::piece(j & 1, 0, h), &maps.k[c.s.part], c.s.g * krow, int(y), bar);
+          if (vbox) tma_load_2d(L::piece(j & 1, 1, h), &maps.v[c.s.part], c.s.g * vrow, int(y), bar);
+        }
+      }
+      // copies still in flight end before the CTA does
+      for (int k = j > 2 ? j - 2 : 0; k < j; ++k)
+        for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(c_full(k), phase(k)); ++i) {
+        }
+    }
+  } else if (warp == kSoftWarps + kFillWarps) {
+    // ---------------------------------------------------------------- products; the warp stays together, one thread issues
     Cursor c(a, range);
     int j = 0, seg = 0;
     bool ok = placed;
-    auto scores = [&](int jj) {
-      const uint32_t d = tmem + uint32_t(L::S + (jj & 1) * TN), k = jj & 1 ? L::K1 : L::K0;
+    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+    auto scores = [&](int jj, bool few) {
+      const uint32_t d = tm + uint32_t(L::S + (jj & 1) * TN);
+      if (elect_one()) {
 #pragma unroll
       for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_f16_ts(d, tmem + uint32_t((part ? L::QL : L::Q) + 8 * ks),
-                        smem_desc_sw128(k + uint32_t(ks >> 2) * (TN * 128) + uint32_t(ks & 3) * 32), L::idesc(TN),
-                        uint32_t(part + ks > 0));
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t k = smem_desc_sw128(L::KT + uint32_t(ks >> 2) * (TN * 128) + uint32_t(ks & 3) * 32);
+          if (few)
+            tc_mma_f16(d, k, smem_desc_sw128(L::QB + uint32_t(part * (D / 64) + (ks >> 2)) * 2048 + uint32_t(ks & 3) * 32),
+                       L::idesc(16), uint32_t(part + ks > 0));
+          else
+            tc_mma_f16_ts(d, tm + uint32_t((part ? L::QL : L::Q) + 8 * ks), k, L::idesc(TN), uint32_t(part + ks > 0));
+        }
       mma_commit(s_full(jj));
+      }
+      __syncwarp();
     };
     while (ok && c.live()) {
       const int tiles = c.s.tiles;
-      ok = wait_for(q_full, uint32_t(seg) & 1u, fail) && wait_for(k_full(j), phase(j), fail);
+      const bool few = D <= 128 && c.s.nrows <= kFewRows;
+      ok = __all_sync(kFull, wait_for(q_full, uint32_t(seg) & 1u, fail) && wait_for(k_full(j), phase(j), fail));
       if (!ok) break;
       tc_fence_after();
-      scores(j);
+      scores(j, few);
       for (int i = 0; i < tiles; ++i, ++j) {
         if (i + 1 < tiles) {
-          ok = wait_for(k_full(j + 1), phase(j + 1), fail) && (j < 1 || wait_for(o_done(j - 1), phase(j - 1), fail));
+          ok = __all_sync(kFull, wait_for(k_full(j + 1), phase(j + 1), fail) &&
+                                     (j < 1 || wait_for(o_done(j - 1), phase(j - 1), fail)));
           if (!ok) break;
           tc_fence_after();
-          scores(j + 1);
+          scores(j + 1, few);
         }
-        ok = wait_for(v_full(j), phase(j), fail) && wait_for(p_full(j), phase(j), fail);
+        ok = __all_sync(kFull, wait_for(v_full(j), phase(j), fail) && wait_for(p_full(j), phase(j), fail));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t p = tmem + uint32_t(L::S + (j & 1) * TN), v = L::V0 + uint32_t(j & 1) * 0x8000u;
+        const uint32_t p = tm + uint32_t(L::S + (j & 1) * TN), v = L::V0 + uint32_t(j & 1) * 0x8000u;
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < TN / 16; ++ks)
-          tc_mma_f16_ts(tmem + uint32_t(L::O), p + uint32_t(8 * ks),
-                        smem_desc_sw128(v + uint32_t(ks >> 2) * (D * 128) + uint32_t(ks & 3) * 32), L::idesc(D),
-                        uint32_t(i > 0 || ks > 0));
+        for (int ks = 0; ks < TN / 16; ++ks) {
+          const uint64_t vd = smem_desc_sw128(v + uint32_t(ks >> 2) * (D * 128) + uint32_t(ks & 3) * 32);
+          if (few)  // for d = 64 the product's rows past 64 are not read
+            tc_mma_f16(tm + uint32_t(L::O), vd,
+                       smem_desc_sw128(L::PT + uint32_t(j & 1) * 4096 + uint32_t(ks >> 2) * 2048 + uint32_t(ks & 3) * 32),
+                       L::idesc(16), uint32_t(i > 0 || ks > 0));
+          else
+            tc_mma_f16_ts(tm + uint32_t(L::O), p + uint32_t(ks < TN / 32 ? 8 * ks : TN / 4 + 8 * ks), vd, L::idesc(D),
+                          uint32_t(i > 0 || ks > 0));
+        }
         mma_commit(o_done(j));
+        }
+        __syncwarp();
       }
       ++seg;
       c.i = tiles - 1;
@@ -576,9 +901,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     }
     // products still in flight end before the tensor memory is given up
     uint64_t* drain = &bars[11];
-    mbar_init(drain, 1);
-    fence_mbarrier_init();
-    mma_commit(drain);
+    if (elect_one()) {
+      mbar_init(drain, 1);
+      fence_mbarrier_init();
+      mma_commit(drain);
+    }
+    __syncwarp();
     for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(drain, 0); ++i) {
     }
   }
@@ -595,7 +923,19 @@ template <int D, bool SPLIT> cudaError_t launch_split(const SharedArgs& a, cudaS
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(Tc<D>::kTotal));
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(unsigned(a.grid)), dim3(kThreads), Tc<D>::kTotal, stream, a);
+  SharedMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const int64_t tokens[2] = {a.prefix, a.batch * a.cap};
+  for (int p = 0; p < 2; ++p) {
+    if (tokens[p] == 0) continue;
+    if (D * a.k_bits / 8 % 16 == 0 &&
+        !head_rows_tensor_map(&maps.k[p], a.k_codes[p], tokens[p], a.hkv, D * a.k_bits / 8, Tc<D>::PR))
+      return cudaErrorNotSupported;
+    if (D * a.v_bits / 8 % 16 == 0 &&
+        !head_rows_tensor_map(&maps.v[p], a.v_codes[p], tokens[p], a.hkv, D * a.v_bits / 8, Tc<D>::PR))
+      return cudaErrorNotSupported;
+  }
+  return launch_pdl(k, dim3(unsigned(a.grid)), dim3(kThreads), Tc<D>::kTotal, stream, a, maps);
 }
 
 }  // namespace

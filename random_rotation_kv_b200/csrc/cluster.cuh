@@ -1,0 +1,64 @@
+// cluster.cuh — thread-block clusters: launch and the few PTX operations that the
+// accumulated-weight and eviction kernels use (distributed shared memory, barrier).
+#pragma once
+
+#include "rrq_device.cuh"
+
+namespace rrq {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster meet; shared-memory writes before it are seen after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The 32-bit word at this CTA's shared address `addr` in the CTA of rank `rank`.
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t v, a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Launch `kernel` in clusters of `size` CTAs along x (up to 16: the opt-in size), with
+// programmatic stream serialization allowed.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, unsigned size, size_t smem,
+                           cudaStream_t stream, Args&&... args) {
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(smem));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = size;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// CTAs per cluster for `rows` rows of `n` tokens each: enough for every SM while a CTA keeps
+// at least `least` tokens, a power of two, at most 16.
+inline unsigned cluster_size(int64_t rows, int64_t n, int64_t least) {
+  unsigned c = 1;
+  while (c < 16 && rows * c * 2 <= 160 && n >= int64_t(c) * 2 * least) c *= 2;
+  return c;
+}
+
+}  // namespace rrq

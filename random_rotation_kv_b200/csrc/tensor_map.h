@@ -104,4 +104,27 @@ inline bool half_box64_tensor_map(CUtensorMap* map, const void* base, int64_t ro
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map over `tokens` rows of `heads` code rows of `row_bytes` bytes (a multiple of 16, at
+// most 128) each, moved in boxes of one head's code row × `box_rows` tokens.  Rows of
+// 32, 64 and 128 bytes use the swizzle of their size (chunk c of row r at chunk
+// c ^ (r >> 2 & 1), c ^ (r >> 1 & 3), c ^ (r & 7)), others none.  Loads fill zeros past the
+// last token.  False if the driver rejects the map.
+inline bool head_rows_tensor_map(CUtensorMap* map, const void* base, int64_t tokens, int heads, int row_bytes,
+                                 int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr || tokens <= 0 || tokens >= (int64_t(1) << 31) || row_bytes % 16 != 0 || row_bytes > 128)
+    return false;
+  const cuuint64_t dims[2] = {cuuint64_t(heads) * cuuint64_t(row_bytes), cuuint64_t(tokens)};
+  const cuuint64_t strides[1] = {cuuint64_t(heads) * cuuint64_t(row_bytes)};
+  const cuuint32_t box[2] = {cuuint32_t(row_bytes), cuuint32_t(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapSwizzle sw = row_bytes == 32    ? CU_TENSOR_MAP_SWIZZLE_32B
+                                : row_bytes == 64  ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                   : CU_TENSOR_MAP_SWIZZLE_NONE;
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace rrq
