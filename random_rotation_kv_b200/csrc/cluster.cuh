@@ -2,6 +2,8 @@
 // accumulated-weight and eviction kernels use (distributed shared memory, barrier).
 #pragma once
 
+#include <atomic>
+
 #include "rrq_device.cuh"
 
 namespace rrq {
@@ -19,8 +21,30 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
   uint32_t v, a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
+}
+
+// Words `addr` of the first `size` (at most 16) CTAs, their loads in flight together; 0 for the others.
+__device__ __forceinline__ void ld_cluster_all(uint32_t addr, int size, uint32_t (&v)[16]) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] = c < size ? ld_cluster(addr, uint32_t(c)) : 0u;
+}
+
+// Lets `kernel` run in clusters of 16 with `smem` bytes, once per device (`done`: a bit per
+// device, one word per kernel).
+template <typename... KArgs>
+cudaError_t allow_clusters(void (*kernel)(KArgs...), int smem, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Launch `kernel` in clusters of `size` CTAs along x (up to 16: the opt-in size), with
@@ -28,14 +52,6 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, unsigned size, size_t smem,
                            cudaStream_t stream, Args&&... args) {
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(smem));
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;

@@ -1,17 +1,20 @@
 // evict.cu — the tokens of a quantised cache that keep their place, and their rows moved
 // together.
 //
-// Selection: one cluster of up to 16 CTAs per (sequence, kv head), each with a run of
-// tokens whose keys it reads once and keeps in shared memory (runs too long for it are
-// read again).  A key is the mass as an unsigned integer of the same order; the sink and
-// the recent tokens have the largest key.  The keep-th largest key is found by radix
-// selection: four passes over 8-bit digits from the top, each a histogram per CTA, the
-// CTAs' histograms summed through distributed shared memory by every CTA for itself.
-// Then every warp counts the keys above and equal to it in its own run of tokens, the
+// Selection: one cluster of up to 16 CTAs per (sequence, kv head); a warp owns a run of 512
+// consecutive tokens of its CTA's tile of 8192, 16 per lane, whose masses stay in registers
+// (runs of several tiles are read again for every pass).  A key is the mass as an unsigned
+// integer of the same order; the sink and the recent tokens have the largest key.  The
+// keep-th largest key is found by radix selection: four passes over 8-bit digits from the
+// top, each a histogram per CTA (eight copies by lane, as few digits are in use and equal
+// ones would queue), the CTAs' histograms summed through distributed shared memory by every
+// CTA for itself.  Then every warp counts the keys above and equal to it in its run, the
 // counts' prefixes give each kept token its slot, and of the equal ones the first are
-// kept; so the order of blocks and atomics never shows in the result.  Moving: a second
-// launch over all SMs copies the rows, several per warp, 16 bytes (8 where rows are not a
-// multiple of 16) per lane; it is bound by memory (2·(d·(kb + vb)/8 + 8) bytes per kept row).
+// kept; so the order of blocks and atomics never shows in the result.  The passes are bound
+// by their four cluster barriers, not by the masses, which are read once.
+// Moving: a second launch over all SMs copies the rows, 128 per block, 16 bytes (8 where rows
+// are not a multiple of 16) per access with the code rows of the new cache written in
+// one run; it is bound by memory (2·(d·(kb + vb)/8 + 8) bytes per kept row).
 #include "cluster.cuh"
 #include "evict.h"
 
@@ -19,7 +22,9 @@ namespace rrq {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int64_t kMaxKeys = 50 * 1024;  // keys a CTA keeps (200 KB)
+constexpr int kPer = 16;                      // tokens per lane and tile
+constexpr int kTile = kThreads * kPer;        // tokens per tile
+constexpr int kCopies = 8;                    // of a histogram
 
 __device__ __forceinline__ int64_t clamp_len(const int32_t* lens, int64_t b, int64_t cap) {
   if (lens == nullptr) return cap;
@@ -34,9 +39,10 @@ __device__ __forceinline__ uint32_t mass_key(float v) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-template <bool KEEP>
+// REG: a CTA's run is one tile, read once.
+template <bool REG>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a, int chunk, int size) {
-  extern __shared__ uint32_t s_keys[];  // [chunk] with KEEP
+  __shared__ uint32_t s_copy[kCopies][256];
   __shared__ uint32_t s_hist[2][256];   // alternating passes: the other one may still be read
   __shared__ uint32_t s_sum[256];
   __shared__ uint32_t s_pick[2];        // digit, how many of its keys are kept
@@ -61,42 +67,55 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     }
     return;
   }
-  auto read_key = [&](int t) {
-    return t0 + t < a.sink || t0 + t >= n - a.recent ? 0xffffffffu : mass_key(__ldg(mass + t));
+  // token i of this lane in the tile at `base`: base + first + 32·i
+  const int first = warp * (kPer * 32) + lane;
+  const int sink = int(a.sink - t0 < 0 ? 0 : a.sink - t0 < chunk ? a.sink - t0 : chunk);  // forced: below it,
+  const int64_t tail = n - a.recent - t0;                                                 // and from it on
+  const int recent = int(tail < 0 ? 0 : tail < chunk ? tail : chunk);
+  float v[kPer];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = base + first + 32 * i;
+      v[i] = t < mine ? __ldg(mass + t) : 0.f;
+    }
   };
-  if constexpr (KEEP) {
-#pragma unroll 4
-    for (int t = tid; t < mine; t += kThreads) s_keys[t] = read_key(t);
-  }
-  auto key_at = [&](int t) { return KEEP ? s_keys[t] : read_key(t); };
-  for (int i = tid; i < 512; i += kThreads) s_hist[i >> 8][i & 255] = 0;
-  __syncthreads();
+  auto key_of = [&](int base, int i) {
+    const int t = base + first + 32 * i;
+    return t < sink || t >= recent ? 0xffffffffu : mass_key(v[i]);
+  };
+  if constexpr (REG) load(0);
+  const int tiles = REG ? 1 : (mine + kTile - 1) / kTile;
 
   uint32_t prefix = 0, need = uint32_t(a.keep);
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
-    uint32_t* hist = s_hist[pass & 1];
-    for (int t = tid; t - lane < mine; t += kThreads) {
-      const uint32_t k = t < mine ? key_at(t) : 0u;
-      const bool in = t < mine && (k & mask) == prefix;
-      const uint32_t dgt = (k >> shift) & 255u;
-      // the first lane's digit is counted once for all that share it: equal masses are common
-      const unsigned live = __ballot_sync(kFull, in);
-      if (live == 0) continue;
-      const int first = __ffs(live) - 1;
-      const uint32_t lead = __shfl_sync(kFull, dgt, first);
-      const unsigned same = __ballot_sync(kFull, in && dgt == lead);
-      if (lane == first) atomicAdd(&hist[dgt], uint32_t(__popc(same)));
-      else if (in && !(same >> lane & 1u)) atomicAdd(&hist[dgt], 1u);
+    for (int i = tid; i < kCopies * 256; i += kThreads) s_copy[i >> 8][i & 255] = 0;
+    __syncthreads();
+    for (int tile = 0; tile < tiles; ++tile) {
+      if constexpr (!REG) load(tile * kTile);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t k = key_of(tile * kTile, i);
+        if (tile * kTile + first + 32 * i < mine && (k & mask) == prefix)
+          atomicAdd(&s_copy[lane & (kCopies - 1)][(k >> shift) & 255u], 1u);
+      }
+    }
+    __syncthreads();
+    if (tid < 256) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) sum += s_copy[c][tid];
+      s_hist[pass & 1][tid] = sum;
     }
     cluster_sync();
     if (tid < 256) {
-      uint32_t sum = 0;
-      const uint32_t at = smem_addr(&hist[tid]);
-      for (int c = 0; c < size; ++c) sum += ld_cluster(at, c);
+      uint32_t h[16], sum = 0;
+      ld_cluster_all(smem_addr(&s_hist[pass & 1][tid]), size, h);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) sum += h[c];
       s_sum[tid] = sum;
-      s_hist[(pass + 1) & 1][tid] = 0;  // its readers met at the barrier above
     }
     __syncthreads();
     if (warp == 0) {
@@ -107,8 +126,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       uint32_t suffix = mysum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_down_sync(kFull, suffix, o);
-        if (lane + o < 32) suffix += v;
+        const uint32_t x = __shfl_down_sync(kFull, suffix, o);
+        if (lane + o < 32) suffix += x;
       }
       uint32_t above = suffix - mysum;
       if (above < need && need <= suffix) {
@@ -127,123 +146,154 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     need = s_pick[1];
   }
 
-  // ---- slots: keys above `prefix`, and the first `need` equal to it, in token order.
-  // Warp w: tokens [w·run, (w + 1)·run) of this CTA's.
-  const int run = (mine + kThreads - 1) / kThreads * 32;
-  const int w0 = warp * run, w1 = w0 + run < mine ? w0 + run : mine;
-  uint32_t above = 0, equal = 0;
-  for (int t = w0; t < w1; t += 32) {
-    const bool in = t + lane < w1;
-    const uint32_t k = in ? key_at(t + lane) : 0u;
-    above += __popc(__ballot_sync(kFull, in && k > prefix));
-    equal += __popc(__ballot_sync(kFull, in && k == prefix));
-  }
-  if (lane == 0) s_warp[0][warp] = above, s_warp[1][warp] = equal;
-  __syncthreads();
-  if (tid < 2) {
-    uint32_t sum = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t v = s_warp[tid][w];
-      s_warp[tid][w] = sum;
-      sum += v;
+  // ---- slots: keys above `prefix`, and the first `need` equal to it, in token order (with
+  // several tiles, each tile's warps one after the other)
+  uint32_t before_a = 0, before_e = 0;  // of the CTAs before this one
+  {
+    uint32_t above = 0, equal = 0;
+    for (int tile = 0; tile < tiles; ++tile) {
+      if constexpr (!REG) load(tile * kTile);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t k = key_of(tile * kTile, i);
+        const bool in = tile * kTile + first + 32 * i < mine;
+        above += __popc(__ballot_sync(kFull, in && k > prefix));
+        equal += __popc(__ballot_sync(kFull, in && k == prefix));
+      }
     }
-    s_count[tid] = sum;
-  }
-  cluster_sync();
-  uint32_t pa = s_warp[0][warp], pe = s_warp[1][warp];
-  for (int c = 0; c < rank; ++c) {
-    pa += ld_cluster(smem_addr(&s_count[0]), c);
-    pe += ld_cluster(smem_addr(&s_count[1]), c);
+    if (lane == 0) s_warp[0][warp] = above, s_warp[1][warp] = equal;
+    __syncthreads();
+    if (tid < 2) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const uint32_t x = s_warp[tid][w];
+        if (REG) s_warp[tid][w] = sum;  // one tile: the warps' prefixes at once
+        sum += x;
+      }
+      s_count[tid] = sum;
+    }
+    cluster_sync();
+    before_a = __reduce_add_sync(kFull, lane < rank ? ld_cluster(smem_addr(&s_count[0]), uint32_t(lane)) : 0u);
+    before_e = __reduce_add_sync(kFull, lane < rank ? ld_cluster(smem_addr(&s_count[1]), uint32_t(lane)) : 0u);
   }
   const unsigned below = (1u << lane) - 1u;
-  for (int t = w0; t < w1; t += 32) {
-    const bool in = t + lane < w1;
-    const uint32_t k = in ? key_at(t + lane) : 0u;
-    const unsigned bg = __ballot_sync(kFull, in && k > prefix), be = __ballot_sync(kFull, in && k == prefix);
-    const uint32_t e = pe + __popc(be & below);
-    if (in && (k > prefix || (k == prefix && e < need))) {
-      const uint32_t slot = pa + __popc(bg & below) + (e < need ? e : need);
-      index[slot] = int32_t(t0 + t + lane);
-      if (out_mass) out_mass[slot] = mass[t + lane];
+  for (int tile = 0; tile < tiles; ++tile) {
+    if constexpr (!REG) {
+      // this tile's counts per warp
+      load(tile * kTile);
+      uint32_t above = 0, equal = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t k = key_of(tile * kTile, i);
+        const bool in = tile * kTile + first + 32 * i < mine;
+        above += __popc(__ballot_sync(kFull, in && k > prefix));
+        equal += __popc(__ballot_sync(kFull, in && k == prefix));
+      }
+      __syncthreads();
+      if (lane == 0) s_warp[0][warp] = above, s_warp[1][warp] = equal;
+      __syncthreads();
     }
-    pa += __popc(bg);
-    pe += __popc(be);
+    uint32_t pa = before_a, pe = before_e;
+    if constexpr (REG) {
+      pa += s_warp[0][warp];
+      pe += s_warp[1][warp];
+    } else {
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) pa += s_warp[0][w], pe += s_warp[1][w];
+        before_a += s_warp[0][w];
+        before_e += s_warp[1][w];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = tile * kTile + first + 32 * i;
+      const uint32_t k = key_of(tile * kTile, i);
+      const bool in = t < mine;
+      const unsigned bg = __ballot_sync(kFull, in && k > prefix), be = __ballot_sync(kFull, in && k == prefix);
+      const uint32_t e = pe + __popc(be & below);
+      if (in && (k > prefix || (k == prefix && e < need))) {
+        const uint32_t slot = pa + __popc(bg & below) + (e < need ? e : need);
+        index[slot] = int32_t(t0 + t);
+        if (out_mass) out_mass[slot] = v[i];
+      }
+      pa += __popc(bg);
+      pe += __popc(be);
+    }
   }
   cluster_sync();  // no CTA leaves while its counts are read
 }
 
-// Rows [kept token][kv head] of every sequence.  U: bytes per copy; `lanes` (a power of two)
-// lanes per row, kRows rows per group of lanes with their loads in flight together.
+// Rows [kept token][kv head] of every sequence, 128 per block and step.  U: bytes per copy.
+constexpr int kMoveThreads = 256, kMoveRows = 128;
 template <typename U>
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, int log2l) {
-  constexpr int kRows = 4;
-  const int tid = threadIdx.x, lanes = 1 << log2l, sub = tid & (lanes - 1);
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+  __shared__ int64_t s_src[kMoveRows];
+  const int tid = threadIdx.x;
   const int ku = a.k_row / int(sizeof(U)), vu = a.v_row / int(sizeof(U));
-  const int per = 256 >> log2l;  // rows per block and step
   pdl_release();
   pdl_wait();
   for (int64_t b = blockIdx.y; b < a.batch; b += gridDim.y) {
     const int64_t n = clamp_len(a.lens, b, a.cap);
     const int64_t rows = (n < a.keep ? n : a.keep) * a.hkv;  // row s·hkv + g of the new cache
-    for (int64_t r0 = int64_t(blockIdx.x) * (per * kRows) + (tid >> log2l); r0 < rows; r0 += int64_t(gridDim.x) * (per * kRows)) {
-      int64_t src[kRows];
+    for (int64_t r0 = int64_t(blockIdx.x) * kMoveRows; r0 < rows; r0 += int64_t(gridDim.x) * kMoveRows) {
+      const int live = int(rows - r0 < kMoveRows ? rows - r0 : kMoveRows);
+      __syncthreads();  // the previous step has read s_src
+      if (tid < live) {
+        const int64_t s = (r0 + tid) / a.hkv;
+        const int64_t g = (r0 + tid) - s * a.hkv;
+        s_src[tid] = (b * a.cap + __ldg(a.index + (b * a.hkv + g) * a.keep + s)) * a.hkv + g;
+      }
+      __syncthreads();
+      const int64_t to = b * a.keep * a.hkv + r0;
+      auto copy = [&](const uint8_t* from, uint8_t* out, int units) {
+        const U* f = reinterpret_cast<const U*>(from);
+        U* o = reinterpret_cast<U*>(out) + to * units;
+        const int total = live * units;
+        for (int i0 = tid; i0 < total; i0 += kMoveThreads * 4) {
+          U w[4];
 #pragma unroll
-      for (int e = 0; e < kRows; ++e) {
-        const int64_t r = r0 + e * per;
-        src[e] = -1;
-        if (r < rows) {
-          const int64_t s = r / a.hkv;
-          const int g = int(r - s * a.hkv);
-          src[e] = (b * a.cap + __ldg(a.index + (b * a.hkv + g) * a.keep + s)) * a.hkv + g;
+          for (int e = 0; e < 4; ++e) {
+            const unsigned i = unsigned(i0 + e * kMoveThreads);
+            if (int(i) < total) w[e] = __ldg(f + s_src[i / unsigned(units)] * units + i % unsigned(units));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i0 + e * kMoveThreads < total) o[i0 + e * kMoveThreads] = w[e];
         }
-      }
-      for (int i = sub; i < ku + vu + 2; i += lanes) {
-        const bool norm = i >= ku + vu;
-        U w[kRows];
-        float f[kRows];
-#pragma unroll
-        for (int e = 0; e < kRows; ++e)
-          if (src[e] >= 0) {
-            if (norm) f[e] = __ldg((i == ku + vu ? a.k_norms : a.v_norms) + src[e]);
-            else if (i < ku) w[e] = __ldg(reinterpret_cast<const U*>(a.k_codes + src[e] * a.k_row) + i);
-            else w[e] = __ldg(reinterpret_cast<const U*>(a.v_codes + src[e] * a.v_row) + (i - ku));
-          }
-#pragma unroll
-        for (int e = 0; e < kRows; ++e)
-          if (src[e] >= 0) {
-            const int64_t r = b * a.keep * a.hkv + r0 + e * per;
-            if (norm) (i == ku + vu ? a.ok_norms : a.ov_norms)[r] = f[e];
-            else if (i < ku) reinterpret_cast<U*>(a.ok_codes + r * a.k_row)[i] = w[e];
-            else reinterpret_cast<U*>(a.ov_codes + r * a.v_row)[i - ku] = w[e];
-          }
-      }
+      };
+      float nu = 0.f;
+      const int r = tid & (kMoveRows - 1);
+      if (r < live) nu = __ldg((tid < kMoveRows ? a.k_norms : a.v_norms) + s_src[r]);
+      copy(a.k_codes, a.ok_codes, ku);
+      copy(a.v_codes, a.ov_codes, vu);
+      if (r < live) (tid < kMoveRows ? a.ok_norms : a.ov_norms)[to + r] = nu;
     }
   }
 }
 
 template <typename U> cudaError_t launch_move(const EvictArgs& a, cudaStream_t stream) {
-  const int units = (a.k_row + a.v_row) / int(sizeof(U)) + 2;
-  int log2l = 2;
-  while (log2l < 5 && (1 << log2l) < units) ++log2l;
   const int64_t most = a.keep < a.cap ? a.keep : a.cap;
-  const int64_t blocks = (most * a.hkv + (1024 >> log2l) - 1) / (1024 >> log2l);
+  const int64_t blocks = (most * a.hkv + kMoveRows - 1) / kMoveRows;
   const unsigned y = unsigned(a.batch < 65535 ? a.batch : 65535);
-  const int64_t fill = (int64_t(148) * 8 + y - 1) / y;
-  auto k = evict_move_kernel<U>;
-  return launch_pdl(k, dim3(unsigned(blocks < fill ? blocks : fill), y), dim3(256), 0, stream, a, log2l);
+  const int64_t fill = (int64_t(148) * 16 + y - 1) / y;
+  return launch_pdl(evict_move_kernel<U>, dim3(unsigned(blocks < fill ? blocks : fill), y), dim3(kMoveThreads), 0, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const int64_t rows = a.batch * a.hkv;
+  // runs of one tile where 16 CTAs give them
   unsigned size = cluster_size(rows, a.cap, 512);
-  while (size < 16 && (a.cap + size - 1) / size > kMaxKeys) size *= 2;
+  while (size < 16 && (a.cap + size - 1) / size > kTile) size *= 2;
   const int64_t chunk = (a.cap + size - 1) / size;
-  const bool keep = chunk <= kMaxKeys;
-  const cudaError_t e = launch_cluster(keep ? evict_select_kernel<true> : evict_select_kernel<false>,
-                                       dim3(unsigned(rows * size)), dim3(kThreads), size, keep ? size_t(chunk) * 4 : 0,
-                                       stream, a, int(chunk), int(size));
+  const bool reg = chunk <= kTile;
+  static std::atomic<uint64_t> done[2];
+  auto k = reg ? evict_select_kernel<true> : evict_select_kernel<false>;
+  cudaError_t e = allow_clusters(k, 0, &done[reg]);
+  if (e != cudaSuccess) return e;
+  e = launch_cluster(k, dim3(unsigned(rows * size)), dim3(kThreads), size, 0, stream, a, int(chunk), int(size));
   if (e != cudaSuccess) return e;
   return a.k_row % 16 == 0 && a.v_row % 16 == 0 ? launch_move<uint4>(a, stream) : launch_move<uint2>(a, stream);
 }
