@@ -427,21 +427,32 @@ def rrq_qjl_matrix(seed: int, d: int, device=None) -> torch.Tensor:
 # plain integers to ctypes and ask torch for the raw stream.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _F32, _U8, _I32, _I64 = torch.float32, torch.uint8, torch.int32, torch.int64
+_HALVES = (torch.float16, torch.bfloat16)
 
 
 def _need(t, name: str, dtype, numel: int, dev: int) -> int:
     """Address of a contiguous CUDA tensor of `numel` elements on device `dev`."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    try:
+        if t.dtype is dtype and t.numel() == numel and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev_tensor(t, name, (dtype,))  # raises what is wrong with the tensor itself
     if t.numel() != numel:
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on another device than the first argument")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on another device than the first argument")
+
+
+def _first(t, name: str, dtypes) -> int:
+    """Device of a call's first tensor, which must be a contiguous CUDA tensor of one of `dtypes`."""
+    try:
+        dev = t.get_device()
+        if dev >= 0 and t.dtype in dtypes and t.is_contiguous():
+            return dev
+    except AttributeError:
+        pass
+    _dev_tensor(t, name, dtypes)
+    raise TypeError(f"{name} must be a CUDA tensor")
 
 
 def _call(name: str, dev: int, *args) -> None:
@@ -452,8 +463,14 @@ def _call(name: str, dev: int, *args) -> None:
     else:
         with torch.cuda.device(dev):
             status = fn(*args, _raw_stream(dev))
-    if status != RRQ_OK:
+    if status:
         raise RRQError(status, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _shared_workspace(dev: int, *shape) -> int:
+    with torch.cuda.device(dev):
+        return rrq_attention_shared_workspace_bytes(*shape)
 
 
 def rrq_attention_shared(q: torch.Tensor, pk_codes, pk_norms, pv_codes, pv_norms, tk_codes, tk_norms,
@@ -470,13 +487,13 @@ def rrq_attention_shared(q: torch.Tensor, pk_codes, pk_norms, pv_codes, pv_norms
     ``workspace``: a uint8 device tensor of at least
     rrq_attention_shared_workspace_bytes(...) bytes, of any content; allocated when none
     is given."""
-    _dev_tensor(q, "q", (torch.float16, torch.bfloat16))
-    if q.dim() != 3 or q.shape[2] != d:
+    dev = _first(q, "q", _HALVES)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
         raise ValueError("q must be [batch, hq, d]")
     if hkv < 1:
         raise ValueError("hkv must be at least 1")
-    batch, hq, _ = q.shape
-    dev = q.get_device()
+    batch, hq, _ = shape
     prefix = cap = 0
     pk = pkn = pv = pvn = tk = tkn = tv = tvn = tl = None
     k_row, v_row = d * k_bits // 8, d * v_bits // 8
@@ -497,16 +514,20 @@ def rrq_attention_shared(q: torch.Tensor, pk_codes, pk_norms, pv_codes, pv_norms
         tl = _need(tail_lens, "tail_lens", _I32, batch, dev)
     if out is None:
         out = torch.empty_like(q)
-    to = _need(out, "out", q.dtype, q.numel(), dev)
+    to = _need(out, "out", q.dtype, batch * hq * d, dev)
     if workspace is None:
-        with torch.cuda.device(dev) if dev != torch.cuda.current_device() else contextlib.nullcontext():
-            need = rrq_attention_shared_workspace_bytes(batch, hq, hkv, d, prefix, cap)
-        workspace = torch.empty(need, dtype=_U8, device=q.device)
+        workspace = torch.empty(_shared_workspace(dev, batch, hq, hkv, d, prefix, cap), dtype=_U8, device=q.device)
     size = workspace.numel()
     ws = _need(workspace, "workspace", _U8, size, dev)
-    kc, vc = _HostFloats(k_codebook), _HostFloats(v_codebook)
+    kc = vc = None  # codebooks: host arrays that live until the call returns
+    if k_codebook is not None:
+        k_host = _HostFloats(k_codebook)
+        kc = k_host.ptr
+    if v_codebook is not None:
+        v_host = _HostFloats(v_codebook)
+        vc = v_host.ptr
     _call("rrq_attention_shared", dev, q.data_ptr(), DTYPE_CODE[q.dtype], batch, hq, pk, pkn, pv, pvn, prefix, tk,
-          tkn, tv, tvn, cap, tl, hkv, d, k_bits, k_seed, kc.ptr, v_bits, v_seed, vc.ptr, scale, ws, size, to)
+          tkn, tv, tvn, cap, tl, hkv, d, k_bits, k_seed, kc, v_bits, v_seed, vc, scale, ws, size, to)
     return out
 
 
@@ -523,15 +544,14 @@ def rrq_attention_mass(scores: torch.Tensor, hkv: int, mass=None, lens=None, dec
 
     ``lens``: int32 [batch] on the device; tokens behind a sequence's length keep their
     mass.  ``mass``: the sums so far, zeros when not given.  ``out`` may be ``mass``."""
-    _dev_tensor(scores, "scores", (_F32,))
+    dev = _first(scores, "scores", (_F32,))
     shape = scores.shape
     if len(shape) not in (2, 3):
         raise ValueError("scores must be [batch, hq, T] or [hq, T]")
     if hkv < 1:
         raise ValueError("hkv must be at least 1")
     batch = shape[0] if len(shape) == 3 else 1
-    hq, t_len = shape[-2:]
-    dev = scores.get_device()
+    hq, t_len = shape[-2], shape[-1]
     if out is None:
         out = torch.empty((batch, hkv, t_len) if len(shape) == 3 else (hkv, t_len), dtype=_F32, device=scores.device)
     n = batch * hkv * t_len
@@ -563,20 +583,20 @@ def rrq_evict(mass: torch.Tensor, lens, keep: int, k_codes: torch.Tensor, k_norm
     [batch], out_mass [batch, hkv, keep], k_codes, k_norms, v_codes, v_norms of capacity
     `keep`).  ``out``: the four arrays of the new cache; entries behind a sequence's new
     length are left as they were (zeros, and -1 in index, where this call allocates)."""
-    _dev_tensor(mass, "mass", (_F32,))
-    if mass.dim() != 3:
+    dev = _first(mass, "mass", (_F32,))
+    shape = mass.shape
+    if len(shape) != 3:
         raise ValueError("mass must be [batch, hkv, cap]")
-    batch, hkv, cap = mass.shape
+    batch, hkv, cap = shape
     if keep < 1:
         raise ValueError("keep must be at least 1")
-    for t_, nm in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-        if t_.dim() != 4 or t_.shape[:3] != (batch, cap, hkv):
-            raise ValueError(f"{nm} must be [batch, cap, hkv, row bytes]")
-    for t_, nm in ((k_norms, "k_norms"), (v_norms, "v_norms")):
-        if t_.shape != (batch, cap, hkv):
-            raise ValueError(f"{nm} must be [batch, cap, hkv]")
-    dev, device = mass.get_device(), mass.device
-    k_row, v_row = k_codes.shape[3], v_codes.shape[3]
+    lead, k_shape, v_shape = (batch, cap, hkv), k_codes.shape, v_codes.shape
+    if len(k_shape) != 4 or len(v_shape) != 4 or k_shape[:3] != lead or v_shape[:3] != lead:
+        raise ValueError("k_codes and v_codes must be [batch, cap, hkv, row bytes]")
+    if k_norms.shape != lead or v_norms.shape != lead:
+        raise ValueError("k_norms and v_norms must be [batch, cap, hkv]")
+    device = mass.device
+    k_row, v_row = k_shape[3], v_shape[3]
     d, k_bits, v_bits = _row_widths(k_row, v_row)
     if index is None:
         index = torch.full((batch, hkv, keep), -1, dtype=_I32, device=device)
@@ -617,15 +637,15 @@ def rrq_rope(x: torch.Tensor, positions: torch.Tensor, freqs, interleaved: bool 
     coordinates of every vector turned, the rest copied; ``inverse`` applies the transposed
     map (the gradient with respect to x).  ``freqs``: radians per position on the host
     (float64, as rrq_rope_frequencies returns them).  ``out`` may be ``x``."""
-    _dev_tensor(x, "x", DTYPE_CODE)
-    if x.dim() != 3:
+    dev = _first(x, "x", DTYPE_CODE)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 3:
         raise ValueError("x must be [n, heads, d]")
-    n, heads, d = x.shape
-    dev = x.get_device()
+    n, heads, d = shape
     fr = np.ascontiguousarray(freqs, dtype=np.float64)
     if out is None:
         out = torch.empty_like(x)
-    _call("rrq_rope", dev, x.data_ptr(), DTYPE_CODE[x.dtype], n, heads, d, 2 * fr.size, int(bool(interleaved)),
+    _call("rrq_rope", dev, x.data_ptr(), DTYPE_CODE[dtype], n, heads, d, 2 * fr.size, int(bool(interleaved)),
           _need(positions, "positions", _I64, n, dev), fr.__array_interface__["data"][0], factor, int(bool(inverse)),
-          _need(out, "out", x.dtype, x.numel(), dev))
+          _need(out, "out", dtype, n * heads * d, dev))
     return out

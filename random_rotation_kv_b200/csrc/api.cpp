@@ -623,9 +623,10 @@ int rrq_rope(const void* x, int dtype, int64_t n, int heads, int d, int rot, int
     return RRQ_ERR_INVALID;
   if (!arr_ok(x, n, 16) || !arr_ok(y, n, 16) || !arr_ok(positions, n, 8)) return RRQ_ERR_INVALID;
   rrq::RopeArgs a;
+  rrq::RopeTurns<rrq::kRopeMaxPairs> f;
   for (int i = 0; i < rot / 2; ++i) {
     if (!(std::fabs(freqs[i]) < 2147483648.0)) return RRQ_ERR_INVALID;
-    a.turns[i] = turns_of(freqs[i]);
+    f.turns[i] = turns_of(freqs[i]);
   }
   if (n == 0) return RRQ_OK;
   a.x = x;
@@ -638,7 +639,8 @@ int rrq_rope(const void* x, int dtype, int64_t n, int heads, int d, int rot, int
   a.interleaved = interleaved;
   a.cos_factor = static_cast<float>(factor);
   a.sin_factor = inverse ? -a.cos_factor : a.cos_factor;
-  return status_of(rrq::launch_rope(a, dtype, as_stream(stream)));
+  std::memset(f.turns + rot / 2, 0, sizeof(uint64_t) * (rrq::kRopeMaxPairs - rot / 2));
+  return status_of(rrq::launch_rope(a, f, dtype, as_stream(stream)));
 }
 
 int rrq_q4_0_rot(const void* x, int x_dtype, int64_t n, int d, uint64_t seed, int rotate,

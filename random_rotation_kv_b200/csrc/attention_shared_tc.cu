@@ -38,6 +38,7 @@
 #include <cstring>
 
 #include "attention_shared.cuh"
+#include "cluster.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
 
@@ -920,8 +921,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 
 template <int D, bool SPLIT> cudaError_t launch_split(const SharedArgs& a, cudaStream_t stream) {
   auto k = shared_tc_kernel<D, SPLIT>;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(Tc<D>::kTotal));
+  static std::atomic<uint64_t> done;
+  const cudaError_t e = allow_kernel(k, int(Tc<D>::kTotal), &done);
   if (e != cudaSuccess) return e;
   SharedMaps maps;
   std::memset(&maps, 0, sizeof(maps));

@@ -31,10 +31,10 @@ __device__ __forceinline__ void ld_cluster_all(uint32_t addr, int size, uint32_t
   for (int c = 0; c < 16; ++c) v[c] = c < size ? ld_cluster(addr, uint32_t(c)) : 0u;
 }
 
-// Lets `kernel` run in clusters of 16 with `smem` bytes, once per device (`done`: a bit per
+// Lets `kernel` run with `smem` bytes and in clusters of 16, once per device (`done`: a bit per
 // device, one word per kernel).
 template <typename... KArgs>
-cudaError_t allow_clusters(void (*kernel)(KArgs...), int smem, std::atomic<uint64_t>* done) {
+cudaError_t allow_kernel(void (*kernel)(KArgs...), int smem, std::atomic<uint64_t>* done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -291,7 +291,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const bool reg = chunk <= kTile;
   static std::atomic<uint64_t> done[2];
   auto k = reg ? evict_select_kernel<true> : evict_select_kernel<false>;
-  cudaError_t e = allow_clusters(k, 0, &done[reg]);
+  cudaError_t e = allow_kernel(k, 0, &done[reg]);
   if (e != cudaSuccess) return e;
   e = launch_cluster(k, dim3(unsigned(rows * size)), dim3(kThreads), size, 0, stream, a, int(chunk), int(size));
   if (e != cudaSuccess) return e;

@@ -257,7 +257,7 @@ cudaError_t launch_attention_mass(const MassArgs& a, cudaStream_t stream) {
   const int i = (keep ? 2 : 0) + (vec ? 1 : 0);
   auto k = keep ? (vec ? mass_kernel<true, true> : mass_kernel<false, true>)
                 : (vec ? mass_kernel<true, false> : mass_kernel<false, false>);
-  const cudaError_t e = allow_clusters(k, int(kMaxSmem), &done[i]);
+  const cudaError_t e = allow_kernel(k, int(kMaxSmem), &done[i]);
   if (e != cudaSuccess) return e;
   return launch_cluster(k, dim3(unsigned(rows * size)), dim3(kThreads), size, smem, stream, a, int(chunk), int(size));
 }

@@ -13,6 +13,8 @@
 // cosine serve every head the thread walks; the heads are spread over more threads only
 // while there are too few tokens to fill the GPU.  Pairs that do not come in eights
 // (rot not a multiple of 16) and addresses off 32 bytes take one pair per thread.
+#include <cstring>
+
 #include "rope.h"
 #include "rrq_device.cuh"
 
@@ -80,13 +82,14 @@ template <typename T, int W> __device__ __forceinline__ void from_float(const fl
 
 // One thread per (token, 16 coordinates, block of `per` heads): eight pairs, or 16 copied
 // coordinates from rot on.  log2u: log2(d / 16) threads per token.
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope8_kernel(const __grid_constant__ RopeArgs a, int log2u, int per) {
+template <typename T, bool INTER, int N>
+__global__ void __launch_bounds__(kThreads) rope8_kernel(const RopeArgs a, const __grid_constant__ RopeTurns<N> f, int log2u,
+                                                         int per) {
   constexpr int W = 8 * Elem<T>::kBytes / 4;  // words of eight elements
-  __shared__ uint64_t s_turns[kRopeMaxPairs];
+  __shared__ uint64_t s_turns[N];
   pdl_release();
   const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < half; i += kThreads) s_turns[i] = a.turns[i];
+  for (int i = threadIdx.x; i < half; i += kThreads) s_turns[i] = f.turns[i];
   __syncthreads();
   pdl_wait();
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
@@ -147,8 +150,8 @@ __global__ void __launch_bounds__(kThreads) rope8_kernel(const __grid_constant__
 }
 
 // One thread per (token, pair or copied coordinate, block of heads).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int hblocks) {
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, const __grid_constant__ RopeTurns<N> f, int hblocks) {
   pdl_release();
   pdl_wait();
   const int half = a.rot / 2, units = half + (a.d - a.rot);  // pairs, then copied coordinates
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       for (int h = h0; h < h1; ++h) y[int64_t(h) * a.d + c] = x[int64_t(h) * a.d + c];
       continue;
     }
-    const float2 cs = turn_of(a.turns[u], a.positions[t], a.cos_factor, a.sin_factor);
+    const float2 cs = turn_of(f.turns[u], a.positions[t], a.cos_factor, a.sin_factor);
     const int ia = a.interleaved ? 2 * u : u, ib = a.interleaved ? 2 * u + 1 : u + half;
     for (int h = h0; h < h1; ++h) {
       const float p = float(x[int64_t(h) * a.d + ia]), q = float(x[int64_t(h) * a.d + ib]);
@@ -183,7 +186,7 @@ int head_blocks(int64_t threads, int heads) {
   return int(hb < heads ? hb : heads);
 }
 
-template <typename T> cudaError_t launch_typed(const RopeArgs& a, cudaStream_t stream) {
+template <typename T, int N> cudaError_t launch_pairs(const RopeArgs& a, const RopeTurns<N>& f, cudaStream_t stream) {
   const bool wide = a.rot % 16 == 0 && (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y)) % 32 == 0;
   if (wide && a.n * (a.d / 16) < (int64_t(1) << 38)) {
     int log2u = 2;
@@ -193,23 +196,31 @@ template <typename T> cudaError_t launch_typed(const RopeArgs& a, cudaStream_t s
     if (hb > 65535) hb = 65535;
     const int per = (a.heads + hb - 1) / hb;
     const dim3 grid(unsigned((threads + kThreads - 1) / kThreads), unsigned((a.heads + per - 1) / per));
-    return launch_pdl(a.interleaved ? rope8_kernel<T, true> : rope8_kernel<T, false>, grid, dim3(kThreads), 0, stream, a,
-                      log2u, per);
+    return launch_pdl(a.interleaved ? rope8_kernel<T, true, N> : rope8_kernel<T, false, N>, grid, dim3(kThreads), 0, stream,
+                      a, f, log2u, per);
   }
   const int units = a.rot / 2 + (a.d - a.rot);
   const int hb = head_blocks(a.n * units, a.heads);
   const int64_t blocks = (a.n * hb * units + kThreads - 1) / kThreads;
-  const int grid = grid_for(reinterpret_cast<const void*>(rope_kernel<T>), kThreads, 0, blocks);
-  return launch_pdl(rope_kernel<T>, grid, kThreads, 0, stream, a, hb);
+  const int grid = grid_for(reinterpret_cast<const void*>(rope_kernel<T, N>), kThreads, 0, blocks);
+  return launch_pdl(rope_kernel<T, N>, grid, kThreads, 0, stream, a, f, hb);
+}
+
+template <typename T>
+cudaError_t launch_typed(const RopeArgs& a, const RopeTurns<kRopeMaxPairs>& f, cudaStream_t stream) {
+  if (a.rot > 128) return launch_pairs<T>(a, f, stream);
+  RopeTurns<64> few;
+  std::memcpy(&few, &f, sizeof(few));
+  return launch_pairs<T>(a, few, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t stream) {
+cudaError_t launch_rope(const RopeArgs& a, const RopeTurns<kRopeMaxPairs>& f, int dtype, cudaStream_t stream) {
   switch (dtype) {
-    case RRQ_F16: return launch_typed<__half>(a, stream);
-    case RRQ_BF16: return launch_typed<__nv_bfloat16>(a, stream);
-    default: return launch_typed<float>(a, stream);
+    case RRQ_F16: return launch_typed<__half>(a, f, stream);
+    case RRQ_BF16: return launch_typed<__nv_bfloat16>(a, f, stream);
+    default: return launch_typed<float>(a, f, stream);
   }
 }
 

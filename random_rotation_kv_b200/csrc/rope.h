@@ -16,9 +16,14 @@ struct RopeArgs {
   int64_t n;
   int heads, d, rot, interleaved;
   float cos_factor, sin_factor;  // factor, and ±factor (− for the transposed map)
-  uint64_t turns[kRopeMaxPairs];  // frequency of pair i in units of 2^-64 turns per position
 };
 
-cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t stream);
+// Frequency of pair i in units of 2^-64 turns per position.  A kernel parameter: launches
+// with the 512 bytes of 64 pairs cost the host less than with 2 KB.
+template <int N> struct RopeTurns {
+  uint64_t turns[N];
+};
+
+cudaError_t launch_rope(const RopeArgs& a, const RopeTurns<kRopeMaxPairs>& f, int dtype, cudaStream_t stream);
 
 }  // namespace rrq
