@@ -348,7 +348,7 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  * rounded to q_dtype.
  * Errors: RRQ_ERR_INVALID (incl. a workspace that is too small), RRQ_ERR_UNSUPPORTED
  * (q_dtype RRQ_F32, more than 128 heads per kv head, 2^31 or more tokens in a cache,
- * 2^30 or more 64-token tiles, or a device whose per-block reserved shared memory is not the 1 KB that the tensor-core
+ * about 10^8 or more 64-token tiles over all kv heads, or a device whose per-block reserved shared memory is not the 1 KB that the tensor-core
  * kernel's layout assumes), RRQ_ERR_CUDA.
  */
 int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,

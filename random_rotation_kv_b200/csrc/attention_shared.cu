@@ -46,31 +46,46 @@ template <int N> __device__ __forceinline__ void fwht_row(float (&v)[N], int lan
 template <int D>
 __global__ void __launch_bounds__(256) shared_prepare_kernel(const SharedArgs a) {
   constexpr int N = D / 32;
-  __shared__ int s_sum[256];
+  __shared__ int2 s_sum[8];
   pdl_release();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x == 0) {
-    int before = 0;
+    int before = 0, filled = 0;
     for (int64_t b0 = 0; b0 < a.batch; b0 += 256) {
       const int64_t b = b0 + tid;
-      const int mine = b < a.batch ? (shared_tail_len(a, b) + a.tile - 1) / a.tile : 0;
-      s_sum[tid] = mine;
-      __syncthreads();
-      for (int o = 1; o < 256; o <<= 1) {
-        const int v = tid >= o ? s_sum[tid - o] : 0;
-        __syncthreads();
-        s_sum[tid] += v;
-        __syncthreads();
+      int len = 0;
+      if (b < a.batch && a.lens) {
+        const int n = a.lens[b];
+        len = n < 0 ? 0 : n > a.cap ? int(a.cap) : n;
       }
-      if (b < a.batch) a.head[kHeadTails + b] = before + s_sum[tid] - mine;
-      before += s_sum[255];
+      const int mine = (len + a.tile - 1) / a.tile;
+      int sum = mine, some = mine > 0;  // inclusive prefixes: of the warp, then of the block
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, sum, o), y = __shfl_up_sync(kFull, some, o);
+        if (lane >= o) sum += x, some += y;
+      }
+      if (lane == 31) s_sum[warp] = make_int2(sum, some);
+      __syncthreads();
+      int all = 0, all_some = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const int2 x = s_sum[w];
+        if (w < warp) sum += x.x, some += x.y;
+        all += x.x;
+        all_some += x.y;
+      }
+      if (b < a.batch) a.tails[b] = make_int4(before + sum - mine, filled + some - (mine > 0), len, mine);
+      before += all;
+      filled += all_some;
       __syncthreads();
     }
     if (tid == 0) {
-      a.head[kHeadTails + a.batch] = before;
+      a.tails[a.batch] = make_int4(before, filled, 0, 0);
       const int total = a.hkv * (a.row_tiles * a.ptiles + before);
-      const int64_t cost = int64_t(a.hkv) * (int64_t(a.row_tiles) * a.ptiles * a.pcost + int64_t(before) * a.tcost);
+      const int64_t cost = int64_t(a.hkv) * (int64_t(a.row_tiles) * a.ptiles * a.pcost + int64_t(before) * a.tcost +
+                                             int64_t(filled) * a.scost);
       const int per = int((cost + a.grid - 1) / a.grid);
       a.head[0] = total;
       a.head[1] = per < a.min_cost ? a.min_cost : per;
@@ -204,17 +219,15 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
   const int64_t b = row / a.hq;
   const int h = int(row % a.hq), g = h / a.group;
   const int64_t r = b * a.group + h % a.group;
-  const int ptotal = a.hkv * a.row_tiles * a.ptiles;
-  int np = 0, nt = 0;
+  int np = 0, nt = 0;  // parts of the prefix, of the tail
   if (a.ptiles > 0) {
     const int first = (g * a.row_tiles + int(r / 128)) * a.ptiles;
-    np = range_of(a, first + a.ptiles - 1) - range_of(a, first) + 1;
+    np = range_of_cost(a, int64_t(first + a.ptiles - 1) * a.pcost) - range_of_cost(a, int64_t(first) * a.pcost) + 1;
   }
-  const int* sums = a.head + kHeadTails;
-  const int tiles = sums[b + 1] - sums[b];
-  if (tiles > 0) {
-    const int first = ptotal + a.hkv * sums[b] + g * tiles;
-    nt = range_of(a, first + tiles - 1) - range_of(a, first) + 1;
+  const int4 tail = a.tails[b];
+  if (tail.w > 0) {
+    const int64_t first = tail_cost(a, tail, g);
+    nt = range_of_cost(a, first + int64_t(tail.w - 1) * a.tcost) - range_of_cost(a, first) + 1;
   }
   auto state = [&](int i) {
     const int p = i < np ? i : a.parts_p + (i - np);
@@ -285,13 +298,15 @@ bool attention_shared_plan(SharedArgs* a) {
   const int64_t pt = (a->prefix + a->tile - 1) / a->tile, tt = (a->cap + a->tile - 1) / a->tile;
   const int64_t punits = int64_t(a->hkv) * a->row_tiles, tunits = int64_t(a->hkv) * a->batch;
   if (tunits == 0) return true;  // no sequence: nothing runs
-  if (pt > most / punits || tt > most / tunits || (punits * pt + tunits * tt) * 4 >= 2 * most) return false;
+  if (pt > most / punits || tt > most / tunits || (punits * pt + tunits * (tt + 1)) >= most / 10) return false;
   a->ptiles = int(pt);
   a->grid = sm_count();
-  // cost of a tile, measured: what fills it, plus the weights of more than 16 rows
-  a->pcost = a->d <= 128 && a->rows <= 16 ? 3 : 4;
-  a->tcost = a->d <= 128 && a->group <= 16 ? 3 : 4;
-  a->min_cost = kMinTiles * 4;
+  // costs, measured: a tile against up to 16 rows 1.7 us, against more 2.5 us, a tail's start
+  // and end 2 us
+  a->pcost = a->d <= 128 && a->rows <= 16 ? 7 : 10;
+  a->tcost = a->d <= 128 && a->group <= 16 ? 7 : 10;
+  a->scost = 8;
+  a->min_cost = kMinTiles * 10;
   int64_t per = (punits * pt * a->pcost + a->grid - 1) / a->grid;  // a range is never shorter
   if (per < a->min_cost) per = a->min_cost;
   auto parts = [per](int64_t tiles, int cost) {
@@ -323,11 +338,12 @@ void attention_shared_levels(SharedArgs* a, bool default_k, bool default_v) {
 
 size_t attention_shared_layout(SharedArgs* a, void* base) {
   const size_t rows = size_t(a->rows) * size_t(a->hkv), parts = size_t(a->parts_p) + size_t(a->parts_t);
-  const size_t head = pad256((kHeadTails + size_t(a->batch) + 1) * 4);
+  const size_t head = pad256(256 + (size_t(a->batch) + 1) * 16);
   const size_t q = pad256(rows * a->d * 4), qe = pad256(rows * 4), st = pad256(parts * rows * 8);
   uint8_t* p = static_cast<uint8_t*>(base);
   if (p != nullptr) {
     a->head = reinterpret_cast<int*>(p);
+    a->tails = reinterpret_cast<int4*>(p + 256);
     a->qrot = reinterpret_cast<float*>(p + head);
     a->qh = reinterpret_cast<__half*>(p + head);
     a->ql = a->qh + rows * a->d;

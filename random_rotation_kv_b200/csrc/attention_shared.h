@@ -15,8 +15,9 @@ namespace rrq {
 // of query rows attends to: the prefix of kv head g with up to 128 rows (row tile rt),
 // or the tail of sequence b at kv head g with its `group` rows.  All units' tiles stand
 // in one line (prefix units first, then the tails by sequence and head), cut into
-// `grid` ranges of equal cost: range c belongs to CTA c, and a unit that crosses
-// ranges leaves one partial state per range, merged at the end.
+// `grid` ranges of equal cost (a cost per tile, and one per tail for its start and end):
+// range c belongs to CTA c, and a unit that crosses ranges leaves one partial state per
+// range, merged at the end.
 struct SharedArgs {
   const void* q;  // [batch × hq × d] fp16 or bf16
   void* out;      // the same
@@ -33,7 +34,8 @@ struct SharedArgs {
   int tile;              // tokens per tile
   int ptiles;            // tiles of the prefix
   int grid;              // ranges
-  int pcost, tcost;      // cost of a tile of the prefix, of a tail; ranges are cut to equal cost
+  int pcost, tcost;      // cost of a tile of the prefix, of a tail
+  int scost;             // of a tail besides its tiles
   int min_cost;          // of a range
   int parts_p, parts_t;  // most ranges that share a prefix unit, a tail unit
   int k_bits, v_bits;
@@ -46,7 +48,8 @@ struct SharedArgs {
   float k_alpha, v_alpha;
   int split;             // queries as two fp16 parts
   // workspace
-  int* head;      // [0] tiles in all, [1] cost per range, [16 + b] tiles of the tails before b (one kv head)
+  int* head;      // [0] tiles in all, [1] cost per range
+  int4* tails;    // entry b: tiles and non-empty tails before b (of one kv head), tokens, tiles; one more behind the last
   float* qrot;    // rotated queries, row (g·rows + r), d values (d = 512), or in their place
   __half* qh;     //   the same as fp16 times a power of two per row,
   __half* ql;     //   what that rounding left, when split,

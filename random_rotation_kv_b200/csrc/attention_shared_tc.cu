@@ -46,13 +46,14 @@ namespace rrq {
 namespace {
 
 constexpr uint32_t kWaitLimit = 1u << 24;  // polls, a few seconds in all
-constexpr int kSoftWarps = 8, kFillWarps = 8, kFill = kFillWarps * 32;
+constexpr int kSoftWarps = 8, kFillWarps = 8;
+constexpr int kFill = 128;  // threads that fill K, and as many that fill V
 constexpr int kFewRows = 16;  // rows of a unit that exchanges the operands' roles
 constexpr int kThreads = (kSoftWarps + kFillWarps + 2) * 32;
 
 template <int D> struct Tc {
   static constexpr int TN = D <= 128 ? 128 : 64;     // tokens per tile
-  static constexpr int OCT = D / 8 * TN / kFill;     // K octets per filling thread
+  static constexpr int TURNS = D / 32 * TN / kFill;  // K: turns of 4 octets per thread (a token's, or half a token's)
   static constexpr int PR = TN / 2;                  // rows of a piece of packed codes
   static constexpr uint32_t TILE = TN * D * 2;       // bytes of a K or V stage
   // shared addresses (the dynamic base is checked to be kBase)
@@ -61,9 +62,11 @@ template <int D> struct Tc {
   static constexpr uint32_t TSLOT = 0x4C0;
   static constexpr uint32_t FAIL = 0x4D0;
   static constexpr uint32_t VMAX = 0x500;            // [4 tiles][4 warps] largest value norm
+  static constexpr uint32_t KMAX = 0x540;            // and key norm
   static constexpr uint32_t NK = 0x800, NV = 0x1000; // [4 tiles][TN] norms
   static constexpr uint32_t PT = 0x2000;             // few rows: weights [2 tiles][2 × 64 tokens][16 rows], swizzled
   static constexpr uint32_t QB = 0x4000;             // few rows: queries [part][64 coordinates][16 rows], swizzled
+  static constexpr uint32_t RS = 0x580;              // few rows: [2 segments][16] powers of two taken out of the queries
   static constexpr uint32_t XCH = 0x6000;            // [2 tiles][2 halves][128 rows] maxima
   // packed codes: eight 4 KB pieces of half a tile's rows, at most 64 (d = 256: 128) bytes each
   static constexpr uint32_t piece(int stage, int v, int half) { return 0x8000u + uint32_t(stage * 4 + v * 2 + half) * 0x1000u; }
@@ -201,38 +204,27 @@ __device__ __forceinline__ uint32_t lds_code(uint32_t addr, int bytes) {
 }
 
 // ---- the filling warps' reads, by code width
-// OCT octets from byte sub·OCT·B of a K row: from a piece (row r), or from global memory.
-template <int D, int B, int OCT>
-__device__ __forceinline__ void read_k(uint32_t piece, int r, int sub, uint32_t (&w)[8]) {
-  constexpr int W = OCT * B / 4, PITCH = D * B / 8;
-  const uint32_t off = uint32_t(sub) * (OCT * B);
-  if constexpr (W % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      const uint4 v = lds_u4(piece + code_at<PITCH>(r, off + 4 * i));
-      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-    }
-  } else if constexpr (W % 2 == 0) {
-#pragma unroll
-    for (int i = 0; i < W; i += 2) {
-      const uint2 v = lds_u2(piece + code_at<PITCH>(r, off + 4 * i));
-      w[i] = v.x, w[i + 1] = v.y;
-    }
+// Four octets (B words) of a K row, number `it`: from a piece (row r), or from global memory.
+template <int D, int B> __device__ __forceinline__ void read_k(uint32_t piece, int r, int it, uint32_t (&w)[4]) {
+  constexpr int PITCH = D * B / 8;
+  const uint32_t off = uint32_t(it) * (4 * B);
+  if constexpr (B == 4) {
+    const uint4 v = lds_u4(piece + code_at<PITCH>(r, off));
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (B == 2) {
+    const uint2 v = lds_u2(piece + code_at<PITCH>(r, off));
+    w[0] = v.x, w[1] = v.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = lds_code(piece + code_at<PITCH>(r, off + 4 * i), 4);
+    for (int i = 0; i < B; ++i) w[i] = lds_code(piece + code_at<PITCH>(r, off + 4 * i), 4);
   }
 }
-template <int B, int OCT> __device__ __forceinline__ void fetch_k(const uint8_t* p, uint32_t (&w)[8]) {
-#pragma unroll
-  for (int i = 0; i < OCT * B / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
-}
-// Octet i of those words as nibbles.
-template <int B> __device__ __forceinline__ uint32_t octet_of(const uint32_t (&w)[8], int i) {
+// Octet i of four, as nibbles.
+template <int B> __device__ __forceinline__ uint32_t octet_of(const uint32_t (&w)[4], int i) {
   if constexpr (B == 4) return w[i];
   const int bit = 8 * B * i, k = bit >> 5, sh = bit & 31;
   uint32_t v = w[k] >> sh;
-  if (sh + 8 * B > 32) v = __funnelshift_r(w[k], w[k + 1 < 8 ? k + 1 : 7], sh);
+  if (sh + 8 * B > 32) v = __funnelshift_r(w[k], w[k + 1 < 4 ? k + 1 : 3], sh);
   return octet_nibbles(v & (B == 3 ? 0xffffffu : B == 2 ? 0xffffu : 0xffu), B);
 }
 // The B bytes of octet o of the 8 tokens of block kb, token 8·kb + (r + kb) mod 8 in w[r]
@@ -260,22 +252,42 @@ template <int B> __device__ __forceinline__ void fetch_v(const uint8_t* p, int r
   }
 }
 
+template <bool SCALE> __device__ __forceinline__ uint32_t times(uint32_t pair, __half2 nu) {
+  if constexpr (!SCALE) return pair;
+  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&pair), nu);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+// The largest of a tile's norms, as the K-filling warps left them.
+template <int TN> __device__ __forceinline__ float tile_max(uint32_t at, int j) {
+  const float4 m = lds_f4(at + uint32_t(j & 3) * 16);
+  return TN == 128 ? fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) : fmaxf(m.x, m.y);
+}
 // Level pair of byte k of `w`; `lane_word` = table | copy of the lane.
 template <int K> __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_word) {
   return lds_u32(__byte_perm(w, lane_word, K == 0 ? 0x7604u : K == 1 ? 0x7614u : K == 2 ? 0x7624u : 0x7634u));
 }
 
-template <int B, int OCT>
-__device__ __forceinline__ void put_k(const uint32_t (&w)[8], uint32_t row, int c0, int tok, uint32_t lane_word) {
+// Four octets of a token's K row, chunks c0 .. c0 + 3 of `row`; SCALE: times `nu`.  All
+// lookups come before the first store: a load is not moved ahead of a store that might alias it.
+template <int B, bool SCALE>
+__device__ __forceinline__ void put_k(const uint32_t (&w)[4], uint32_t row, int c0, int n, uint32_t lane_word, __half2 nu) {
+  uint32_t p[4][4];
 #pragma unroll
-  for (int i = 0; i < OCT; ++i) {
-    const uint32_t n = octet_of<B>(w, i);
-    sts_v4(row + (uint32_t((c0 + i) ^ (tok & 7)) << 4), pair_of<0>(n, lane_word), pair_of<1>(n, lane_word),
-           pair_of<2>(n, lane_word), pair_of<3>(n, lane_word));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = octet_of<B>(w, i);
+    p[i][0] = pair_of<0>(x, lane_word), p[i][1] = pair_of<1>(x, lane_word);
+    p[i][2] = pair_of<2>(x, lane_word), p[i][3] = pair_of<3>(x, lane_word);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    sts_v4(row + (uint32_t((c0 + i) ^ (n & 7)) << 4), times<SCALE>(p[i][0], nu), times<SCALE>(p[i][1], nu),
+           times<SCALE>(p[i][2], nu), times<SCALE>(p[i][3], nu));
 }
-template <int B>
-__device__ __forceinline__ void put_v(const uint32_t (&w)[16], int o, uint32_t row, int kb, uint32_t lane_word) {
+// Octet o of eight tokens of V, rows 8·o + i, chunk kb; SCALE: times the tokens' `nu` (pairs).
+// Two coordinates per turn of a rolled loop: the filling code stays in the instruction cache.
+template <int B, bool SCALE>
+__device__ __forceinline__ void put_v(const uint32_t (&w)[16], int o, uint32_t row, int kb, uint32_t lane_word,
+                                      const __half2 (&nu)[4]) {
   uint32_t n[8], ev[4], od[4];
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
@@ -289,19 +301,21 @@ __device__ __forceinline__ void put_v(const uint32_t (&w)[16], int o, uint32_t r
     ev[q] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);  // coordinates 0, 2, 4, 6 of two tokens
     od[q] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);  // 1, 3, 5, 7
   }
-  auto put = [&](int i, auto k, const uint32_t (&e)[4]) {
-    constexpr int K = decltype(k)::value;
-    sts_v4(row + uint32_t(i) * 128 + (uint32_t(kb ^ i) << 4), pair_of<K>(e[0], lane_word), pair_of<K>(e[1], lane_word),
-           pair_of<K>(e[2], lane_word), pair_of<K>(e[3], lane_word));
-  };
-  put(0, std::integral_constant<int, 0>{}, ev);
-  put(1, std::integral_constant<int, 0>{}, od);
-  put(2, std::integral_constant<int, 1>{}, ev);
-  put(3, std::integral_constant<int, 1>{}, od);
-  put(4, std::integral_constant<int, 2>{}, ev);
-  put(5, std::integral_constant<int, 2>{}, od);
-  put(6, std::integral_constant<int, 3>{}, ev);
-  put(7, std::integral_constant<int, 3>{}, od);
+#pragma unroll 1
+  for (int i = 0; i < 8; i += 2) {
+    uint32_t p[4], r[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      p[q] = pair_of<0>(ev[q], lane_word);
+      r[q] = pair_of<0>(od[q], lane_word);
+      ev[q] >>= 8;
+      od[q] >>= 8;
+    }
+    sts_v4(row + uint32_t(i) * 128 + (uint32_t(kb ^ i) << 4), times<SCALE>(p[0], nu[0]), times<SCALE>(p[1], nu[1]),
+           times<SCALE>(p[2], nu[2]), times<SCALE>(p[3], nu[3]));
+    sts_v4(row + uint32_t(i + 1) * 128 + (uint32_t(kb ^ (i + 1)) << 4), times<SCALE>(r[0], nu[0]), times<SCALE>(r[1], nu[1]),
+           times<SCALE>(r[2], nu[2]), times<SCALE>(r[3], nu[3]));
+  }
 }
 
 // Columns [h, h + 32) of a tile: `v` where the column's token is not one of the first `valid`.
@@ -314,25 +328,70 @@ __device__ __forceinline__ void mask(float2 (&y)[16], int h, int valid, float v)
   }
 }
 
-// Position in a range, one tile at a time.
+// Finding a place in the line takes searches and 64-bit divisions; out of line, as five
+// roles do it once, and the tiles' code has to stay in the instruction cache.
+__device__ __noinline__ void find_segment(const SharedArgs& a, int range, int pos, int end, Segment* s) {
+  *s = segment_at(a, range, pos, end);
+}
+__device__ __noinline__ void find_range(const SharedArgs& a, int range, int* pos, int* end) {
+  range_tiles(a, range, pos, end);
+}
+
+// Position in a range, one tile at a time.  The segments after the first begin with their
+// unit, so they follow without a search (but for tails of length 0); the next tail's
+// entry is read one sequence ahead.
 struct Cursor {
   int range, pos, end, i;
+  int4 ahead;  // entry of the sequence after this tail's
   Segment s;
   __device__ __forceinline__ Cursor(const SharedArgs& a, int r) : range(r), i(0) {
-    range_tiles(a, r, &pos, &end);
-    if (pos < end) s = segment_at(a, range, pos, end);
+    int p, e;
+    find_range(a, r, &p, &e);
+    pos = p;
+    end = e;
+    if (pos < end) seek(a);
   }
+  __device__ __forceinline__ void seek(const SharedArgs& a) {
+    Segment t;
+    find_segment(a, range, pos, end, &t);
+    s = t;
+    entry = a.tails[s.part ? s.b : 0];
+    ahead = a.tails[s.part ? s.b + 1 : 0];
+  }
+  int4 entry;  // of this tail's sequence
   __device__ __forceinline__ bool live() const { return pos < end; }
   __device__ __forceinline__ void next(const SharedArgs& a) {
-    if (++i == s.tiles) {
-      pos += s.tiles;
-      i = 0;
-      if (pos < end) s = segment_at(a, range, pos, end);
+    if (++i < s.tiles) return;
+    pos += s.tiles;
+    i = 0;
+    if (pos >= end) return;
+    if (s.part == 0) {
+      const int rt = s.b + 1 < a.row_tiles ? s.b + 1 : 0, g = s.g + (rt == 0);
+      if (g == a.hkv) {
+        seek(a);
+        return;
+      }
+      prefix_unit(a, g, rt, &s);
+      cut_segment(a, 0, a.ptiles, a.prefix, end - pos, 0, &s);
+    } else {
+      int g = s.g + 1;
+      int64_t b = s.b;
+      if (g == a.hkv) {
+        if (ahead.w == 0) {
+          seek(a);
+          return;
+        }
+        g = 0;
+        entry = ahead;
+        ahead = a.tails[++b + 1];
+      }
+      tail_unit(a, g, b, &s);
+      cut_segment(a, 0, entry.w, entry.z, end - pos, 0, &s);
     }
   }
 };
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, bool FOLD>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ SharedMaps maps) {
   using L = Tc<D>;
   constexpr int TN = L::TN;
@@ -358,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   if (tid == 0) {
     mbar_init(q_full, kSoftWarps);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(k_full(s), kFillWarps);
-      mbar_init(v_full(s), kFillWarps);
+      mbar_init(k_full(s), kFillWarps / 2);
+      mbar_init(v_full(s), kFillWarps / 2);
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), kSoftWarps);
       mbar_init(o_done(s), 1);
@@ -394,36 +453,39 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const int ln = 32 * quarter + lane;              // this thread's tensor-memory lane
     const uint32_t tl = tmem + (uint32_t(32 * quarter) << 16);
     Cursor c(a, range);
-    int j = 0;
+    int j = 0, seg = 0;
+    bool staged = false;  // the segment's queries are in shared memory already
+    // few rows: the queries of a segment as an operand, rows past its own as zeros
+    auto stage = [&](const Segment& s, int number) {
+      const int64_t qrow = int64_t(s.g) * a.rows + s.row0;
+      const int r = (tid >> 3) & 15, k0 = (tid & 7) + ((tid >> 7) << 3);  // row, chunk of 8 coordinates
+#pragma unroll
+      for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+        if (k0 < D / 8) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (r < s.nrows) v = __ldcg(reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + (qrow + r) * D) + k0);
+          sts_v4(L::QB + uint32_t(part * (D / 64) + (k0 >> 3)) * 2048 + uint32_t(r) * 128 + (uint32_t((k0 ^ r) & 7) << 4), v.x, v.y,
+                 v.z, v.w);
+        }
+      if (tid < 16)
+        *reinterpret_cast<float*>(at(L::RS + uint32_t(number & 1) * 64 + uint32_t(tid) * 4)) = tid < s.nrows ? __ldcg(a.qexp + qrow + tid) : 1.f;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
     while (c.live()) {
       const Segment& s = c.s;
       bool ok = *fail == 0;
       if (D <= 128 && s.nrows <= kFewRows) {
         if constexpr (D <= 128) {
           // ---- few rows: lane = token, columns = rows; this half's rows [8·half, + 8)
-          const int64_t qrow = int64_t(s.g) * a.rows + s.row0;
-          {
-            const int r = (tid >> 3) & 15, k0 = (tid & 7) + ((tid >> 7) << 3);  // row, chunk of 8 coordinates
-#pragma unroll
-            for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
-              if (k0 < D / 8) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < s.nrows) v = __ldcg(reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + (qrow + r) * D) + k0);
-                sts_v4(L::QB + uint32_t(part * (D / 64) + (k0 >> 3)) * 2048 + uint32_t(r) * 128 + (uint32_t((k0 ^ r) & 7) << 4),
-                       v.x, v.y, v.z, v.w);
-              }
-          }
-          fence_proxy_async_smem();
           const bool mine = 8 * half < s.nrows;
+          if (!staged) stage(s, seg);
+          staged = false;
           float rs[8], m[8], mp[8], l[8];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            rs[r] = 8 * half + r < s.nrows ? a.qexp[qrow + 8 * half + r] : 1.f;
-            m[r] = mp[r] = l[r] = 0.f;
-          }
+          for (int r = 0; r < 8; ++r) m[r] = mp[r] = l[r] = 0.f;
           float vn = 0.f;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full);
           for (int i = 0; i < s.tiles; ++i, ++j) {
             ok = ok && wait_for(s_full(j), phase(j), fail);
             ok = __all_sync(kFull, ok);
@@ -439,6 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                 const float nk = __uint_as_float(lds_code(L::NK + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4, 4));
                 nv = __uint_as_float(lds_code(L::NV + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4, 4));
                 tmem_ld_wait();
+                if (i == 0) {
+                  const float4 r0 = lds_f4(L::RS + uint32_t(seg & 1) * 64 + uint32_t(half) * 32);
+                  const float4 r1 = lds_f4(L::RS + uint32_t(seg & 1) * 64 + uint32_t(half) * 32 + 16);
+                  rs[0] = r0.x, rs[1] = r0.y, rs[2] = r0.z, rs[3] = r0.w, rs[4] = r1.x, rs[5] = r1.y, rs[6] = r1.z, rs[7] = r1.w;
+                }
                 float mx[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
@@ -460,8 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 #pragma unroll
                   for (int r = 0; r < 8; ++r) mx[r] = q ? fmaxf(mx[r], x[r]) : x[r];
                 }
-                const float4 vm = lds_f4(L::VMAX + uint32_t(j & 3) * 16);
-                const float pw = norm_unit(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)));
+                const float pw = norm_unit(tile_max<TN>(L::VMAX, j));
                 if (i == 0) {
                   vn = pw;
 #pragma unroll
@@ -510,6 +576,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full(j));
           }
+          // the next segment's queries go in while this one's last product runs: S of all its
+          // tiles is done
+          const Segment done = s;
+          c.i = s.tiles - 1;
+          c.next(a);
+          if (c.live() && c.s.nrows <= kFewRows) {
+            stage(c.s, seg + 1);
+            staged = true;
+          }
           ok = ok && wait_for(o_done(j - 1), phase(j - 1), fail);
           ok = __all_sync(kFull, ok);
           tc_fence_after();
@@ -525,14 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               sts_v4(wl + uint32_t(quarter) * 32 + 16, __float_as_uint(l[4]), __float_as_uint(l[5]), __float_as_uint(l[6]), __float_as_uint(l[7]));
             }
             ok = meet(uint32_t(5 + half), 128, ok);
-            if (quarter == 0 && lane < 8 && 8 * half + lane < s.nrows) {
+            if (quarter == 0 && lane < 8 && 8 * half + lane < done.nrows) {
               float sum = 0.f, mine_mp = mp[0];
 #pragma unroll
               for (int q = 0; q < 4; ++q) sum += __uint_as_float(lds_code(wl + uint32_t(q) * 32 + uint32_t(lane) * 4, 4));
 #pragma unroll
               for (int r = 1; r < 8; ++r)
                 if (lane == r) mine_mp = mp[r];
-              a.stats[s.state + 8 * half + lane] = ok ? make_float2(mine_mp, sum) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
+              a.stats[done.state + 8 * half + lane] = ok ? make_float2(mine_mp, sum) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
             }
             if (ok) {
               uint32_t o[8];
@@ -540,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               tmem_ld_wait();
 #pragma unroll
               for (int r = 0; r < 8; ++r)
-                if (8 * half + r < s.nrows && ln < D) a.acc[(s.state + 8 * half + r) * D + ln] = __uint_as_float(o[r]);
+                if (8 * half + r < done.nrows && ln < D) a.acc[(done.state + 8 * half + r) * D + ln] = __uint_as_float(o[r]);
             }
             // the next segment writes this slot of the exchange again
             meet(uint32_t(5 + half), 128, true);
@@ -575,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         if (lane == 0) mbar_arrive(q_full);
 
         float m = 0.f, mp = 0.f, vn = 0.f;  // running maximum, m', N
-        float2 l2 = make_float2(0.f, 0.f), l3 = l2;
+        float l = 0.f;
         const uint32_t pair = uint32_t(1 + quarter);
         for (int i = 0; i < s.tiles; ++i, ++j) {
           ok = ok && wait_for(s_full(j), phase(j), fail);
@@ -590,31 +665,40 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             const uint32_t xch = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(ln) * 4;
             float mx = -INFINITY;
             if (ok) {
-              // the largest ν^K·S of the row's half (loops kept rolled: unrolled, the warps'
+              // the largest score of the row's half (loops kept rolled: unrolled, the warps'
               // different code ran out of the instruction cache)
+              auto largest = [&](auto whole) {
 #pragma unroll 1
-              for (int h = 0; h < TH; h += 32) {
-                uint32_t v[32];
-                tmem_ld32(sb + h, v);
-                tmem_ld_wait();
-                float2 y[16];
+                for (int h = 0; h < TH; h += 32) {
+                  uint32_t v[32];
+                  tmem_ld32(sb + h, v);
+                  tmem_ld_wait();
+                  float2 y[16];
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                  const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
-                  y[k / 2] = mul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), make_float2(n.x, n.y));
-                  y[k / 2 + 1] = mul2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), make_float2(n.z, n.w));
+                  for (int k = 0; k < 32; k += 4) {
+                    y[k / 2] = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                    y[k / 2 + 1] = make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+                    if constexpr (!FOLD) {
+                      const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
+                      y[k / 2] = mul2(y[k / 2], make_float2(n.x, n.y));
+                      y[k / 2 + 1] = mul2(y[k / 2 + 1], make_float2(n.z, n.w));
+                    }
+                  }
+                  if constexpr (!decltype(whole)::value) mask(y, half * TH + h, valid, -INFINITY);
+#pragma unroll
+                  for (int k = 0; k < 16; k += 2) mx = fmaxf(mx, fmaxf(fmaxf(y[k].x, y[k].y), fmaxf(y[k + 1].x, y[k + 1].y)));
                 }
-                if (!full) mask(y, half * TH + h, valid, -INFINITY);
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) mx = fmaxf(mx, fmaxf(fmaxf(y[k].x, y[k].y), fmaxf(y[k + 1].x, y[k + 1].y)));
-              }
+              };
+              if (full) largest(std::true_type{});
+              else largest(std::false_type{});
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + uint32_t(half) * 512), "f"(mx) : "memory");
             }
             ok = meet(pair, 64, ok);
             if (ok) {
-              mx = fmaxf(mx, __uint_as_float(lds_code(xch + uint32_t(half ^ 1) * 512, 4))) * rs;
-              const float4 vm = lds_f4(L::VMAX + uint32_t(j & 3) * 16);
-              const float pw = norm_unit(TN == 128 ? fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)) : fmaxf(vm.x, vm.y));
+              // 2^e, times the unit of the tile's key norms where these are in K already
+              const float rj = FOLD ? rs * norm_unit(tile_max<TN>(L::KMAX, j)) : rs;
+              mx = fmaxf(mx, __uint_as_float(lds_code(xch + uint32_t(half ^ 1) * 512, 4))) * rj;
+              const float pw = norm_unit(tile_max<TN>(L::VMAX, j));
               if (i == 0) {
                 m = mx;
                 vn = pw;
@@ -626,8 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                   if (wide) vn = pw;
                   const float mn = shifted(m, vn), f = ex2(mp - mn);
                   mp = mn;
-                  l2 = mul2(l2, make_float2(f, f));
-                  l3 = mul2(l3, make_float2(f, f));
+                  l *= f;
                   ok = __all_sync(kFull, wait_for(o_done(j - 1), phase(j - 1), fail));
                   tc_fence_after();
 #pragma unroll 1
@@ -642,36 +725,55 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                   tmem_st_wait();
                 }
               }
-              // weights into S's columns, the sum of the exponentials
-              const float2 rs2 = make_float2(rs, rs), mp2 = make_float2(-mp, -mp);
+              // weights into S's columns, the sum of the exponentials; with the value norms (over
+              // their unit pw) in V already, the weights carry pw and the sum is freed of it
+              const float mj = FOLD ? mp - float(int(__float_as_uint(pw) >> 23) - 127) : mp;
+              const float2 rs2 = make_float2(rj, rj), mp2 = make_float2(-mj, -mj);
               const uint32_t pb = sb;  // the first half of the columns that this thread reads
+              float2 s2 = make_float2(0.f, 0.f), s3 = s2;
+              auto weigh = [&](auto whole) {
 #pragma unroll 1
-              for (int h = 0; h < TH; h += 32) {
-                uint32_t v[32], p[16];
-                tmem_ld32(sb + h, v);
-                tmem_ld_wait();
-                float2 e[16];
+                for (int h = 0; h < TH; h += 32) {
+                  uint32_t v[32], p[16];
+                  tmem_ld32(sb + h, v);
+                  tmem_ld_wait();
+                  float2 e[16];
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                  const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
-                  const float2 x0 = fma2(mul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), make_float2(n.x, n.y)), rs2, mp2);
-                  const float2 x1 = fma2(mul2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), make_float2(n.z, n.w)), rs2, mp2);
-                  e[k / 2] = make_float2(ex2(x0.x), ex2(x0.y));
-                  e[k / 2 + 1] = make_float2(ex2(x1.x), ex2(x1.y));
-                }
-                if (!full) mask(e, half * TH + h, valid, 0.f);
+                  for (int k = 0; k < 32; k += 4) {
+                    float2 x0 = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                    float2 x1 = make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+                    if constexpr (!FOLD) {
+                      const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
+                      x0 = mul2(x0, make_float2(n.x, n.y));
+                      x1 = mul2(x1, make_float2(n.z, n.w));
+                    }
+                    x0 = fma2(x0, rs2, mp2);
+                    x1 = fma2(x1, rs2, mp2);
+                    e[k / 2] = make_float2(ex2(x0.x), ex2(x0.y));
+                    e[k / 2 + 1] = make_float2(ex2(x1.x), ex2(x1.y));
+                  }
+                  if constexpr (!decltype(whole)::value) mask(e, half * TH + h, valid, 0.f);
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                  const float4 w = lds_f4(nv + uint32_t(h + k) * 4);
-                  l2 = add2(l2, e[k / 2]);
-                  l3 = add2(l3, e[k / 2 + 1]);
-                  const float2 w0 = mul2(e[k / 2], make_float2(w.x, w.y)), w1 = mul2(e[k / 2 + 1], make_float2(w.z, w.w));
-                  const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
-                  p[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-                  p[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                  for (int k = 0; k < 32; k += 4) {
+                    float2 w0 = e[k / 2], w1 = e[k / 2 + 1];
+                    s2 = add2(s2, w0);
+                    s3 = add2(s3, w1);
+                    if constexpr (!FOLD) {
+                      const float4 w = lds_f4(nv + uint32_t(h + k) * 4);
+                      w0 = mul2(w0, make_float2(w.x, w.y));
+                      w1 = mul2(w1, make_float2(w.z, w.w));
+                    }
+                    const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
+                    p[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+                    p[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                  }
+                  tmem_st16(pb + h / 2, p);
                 }
-                tmem_st16(pb + h / 2, p);
-              }
+              };
+              if (full) weigh(std::true_type{});
+              else weigh(std::false_type{});
+              const float u = FOLD ? 1.f / pw : 1.f;  // a power of two
+              l += u * ((s2.x + s2.y) + (s3.x + s3.y));
               tmem_st_wait();
             }
           }
@@ -685,12 +787,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         tc_fence_after();
         if (warp_ok) {
           const uint32_t xch = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(ln) * 4;
-          const float sum = (l2.x + l2.y) + (l3.x + l3.y);
-          if (half) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch), "f"(sum) : "memory");
+          if (half) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch), "f"(l) : "memory");
           ok = meet(pair, 64, ok);
           const int64_t st = s.state + ln;
           if (!half && row_ok)
-            a.stats[st] = ok ? make_float2(mp, sum + __uint_as_float(lds_code(xch, 4))) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
+            a.stats[st] = ok ? make_float2(mp, l + __uint_as_float(lds_code(xch, 4))) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
           if (ok) {
 #pragma unroll 1
             for (int k = 0; k < DH; k += 32) {
@@ -709,107 +810,159 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           }
           meet(pair, 64, true);  // the next segment writes this slot of the exchange again
         }
+        c.i = s.tiles - 1;
+        c.next(a);
       }
-      c.i = s.tiles - 1;
-      c.next(a);
+      ++seg;
     }
   } else if (warp < kSoftWarps + kFillWarps) {
     // ------------------------------------------------------------ codes to fp16 levels in shared memory
-    const int ft = tid - kSoftWarps * 32;
-    const int n = ft % TN, sub = ft / TN;                 // K: row n, OCT octets from sub·OCT
-    const int tok = token_of(n);                          // its token
-    const int c0 = (sub * L::OCT) & 7, kblock = sub * L::OCT / 8;
-    const int kb = lane & 7, rest = ft >> 3;              // V: 8 tokens, one octet
-    const int vo = rest % (D / 8), vblock = rest / (D / 8);
-    const bool v_mine = vblock < TN / 64;
-    const int v_tok = 64 * vblock + 8 * kb;
-    const uint32_t kword = L::TABLE | uint32_t(lane * 4), vword = kword | 128u;
-    const uint32_t krow = uint32_t(kblock) * (TN * 128) + uint32_t(n) * 128;
-    const uint32_t vrow = uint32_t(vblock) * (D * 128) + uint32_t(8 * vo) * 128;
-    uint32_t kw[8], vw[16];
-    float norm_k = 0.f, norm_v = 0.f;
-    // what comes from global memory for the cursor's tile: norms, and rows no box can move
-    auto fetch = [&](const Cursor& c) {
-      const Segment& s = c.s;
-      auto row_of = [&](int t) {
-        const int64_t tt = s.t0 + int64_t(c.i) * TN + t;
-        return (s.token_base + (tt < s.t1 ? tt : s.t1 - 1)) * a.hkv + s.g;
-      };
-      const int64_t row = row_of(tok);
-      if (sub == 0) {
-        norm_k = __ldg(a.k_norms[s.part] + row);
-        norm_v = s.t0 + int64_t(c.i) * TN + tok < s.t1 ? __ldg(a.v_norms[s.part] + row) : 0.f;
-      }
-      if constexpr (D == 64) {
-        const uint8_t* kc = a.k_codes[s.part] + row * (D * a.k_bits / 8) + sub * L::OCT * a.k_bits;
-        if (a.k_bits == 1) fetch_k<1, L::OCT>(kc, kw);
-        else if (a.k_bits == 3) fetch_k<3, L::OCT>(kc, kw);
-        if (v_mine && (a.v_bits & 1)) {
+    const int ft = (tid - kSoftWarps * 32) & (kFill - 1);
+    const bool v_side = warp >= kSoftWarps + kFillWarps / 2;
+    const uint32_t lane_word = L::TABLE | uint32_t(lane * 4) | (v_side ? 128u : 0u);
+    // row of the cache of a tile's token t; rows past the segment's end repeat its last
+    auto row_of = [&](const Cursor& c, int t) {
+      const int64_t tt = c.s.t0 + int64_t(c.i) * TN + t;
+      return (c.s.token_base + (tt < c.s.t1 ? tt : c.s.t1 - 1)) * a.hkv + c.s.g;
+    };
+    auto folded = [&](const Cursor& c) { return FOLD && !(D <= 128 && c.s.nrows <= kFewRows); };
+    Cursor c(a, range);
+    bool ok = placed;
+    if (!v_side) {
+      // ---- K: one token per thread (half of one for d = 256), and the tile's norms
+      const int n = ft % TN, sub = ft / TN;  // row of the tile
+      const int tok = token_of(n);
+      uint32_t kw[2][4];  // rows that no box moves (d = 64)
+      float norm_k = 0.f, norm_v = 0.f;
+      auto fetch = [&] {  // what comes from global memory for the cursor's tile
+        const int64_t row = row_of(c, tok);
+        norm_k = __ldg(a.k_norms[c.s.part] + row);
+        norm_v = c.s.t0 + int64_t(c.i) * TN + tok < c.s.t1 ? __ldg(a.v_norms[c.s.part] + row) : 0.f;
+        if constexpr (D == 64) {
+          const uint8_t* kc = a.k_codes[c.s.part] + row * (D * a.k_bits / 8);
+          if (a.k_bits & 1) {
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const uint8_t* vc = a.v_codes[s.part] + row_of(v_tok + ((r + kb) & 7)) * (D * a.v_bits / 8);
-            if (a.v_bits == 1) fetch_v<1>(vc, r, vo, vw);
-            else fetch_v<3>(vc, r, vo, vw);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+                if (k < a.k_bits) kw[i][k] = __ldg(reinterpret_cast<const uint32_t*>(kc) + i * a.k_bits + k);
           }
         }
-      }
-    };
-    auto fill_k = [&](auto bits, int j) {
-      constexpr int B = decltype(bits)::value;
-      if constexpr (kBoxed<D, B>) read_k<D, B, L::OCT>(L::piece(j & 1, 0, tok / L::PR), tok % L::PR, sub, kw);
-      put_k<B, L::OCT>(kw, L::KT + krow, c0, n, kword);
-    };
-    auto fill_v = [&](auto bits, int j) {
-      constexpr int B = decltype(bits)::value;
-      if constexpr (kBoxed<D, B>) read_v<D, B>(L::piece(j & 1, 1, v_tok / L::PR), v_tok % L::PR, kb, vo, vw);
-      put_v<B>(vw, vo, L::V0 + uint32_t(j & 1) * 0x8000u + vrow, kb, vword);
-    };
-    Cursor c(a, range);
-    if (c.live()) fetch(c);
-    bool ok = placed;
-    for (int j = 0; c.live(); ++j) {
-      ok = ok && wait_for(c_full(j), phase(j), fail);
-      if (j >= 1) ok = ok && wait_for(s_full(j - 1), phase(j - 1), fail);
-      ok = __all_sync(kFull, ok);
-      if (!ok) break;
-      // the slot's last reader was tile j − 4: its weights were made before S of tile j − 1 began
-      if (sub == 0) {
+      };
+      if (c.live()) fetch();
+      for (int j = 0; c.live(); ++j) {
+        // norm slots are used every fourth tile: what read this one before was done when S
+        // of tile j − 2 began
         const uint32_t slot = uint32_t(j & 3) * (TN * 4) + uint32_t(n) * 4;
-        *reinterpret_cast<float*>(at(L::NK + slot)) = norm_k;
-        *reinterpret_cast<float*>(at(L::NV + slot)) = norm_v;
-        float big = norm_v;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-        if (lane == 0) *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = big;
-      }
-      switch (a.k_bits) {
-        case 1: fill_k(std::integral_constant<int, 1>{}, j); break;
-        case 2: fill_k(std::integral_constant<int, 2>{}, j); break;
-        case 3: fill_k(std::integral_constant<int, 3>{}, j); break;
-        default: fill_k(std::integral_constant<int, 4>{}, j); break;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(k_full(j));
-      if (j >= 2) ok = wait_for(o_done(j), phase(j - 2), fail);
-      ok = __all_sync(kFull, ok);
-      if (!ok) break;
-      if (v_mine) {
-        switch (a.v_bits) {
-          case 1: fill_v(std::integral_constant<int, 1>{}, j); break;
-          case 2: fill_v(std::integral_constant<int, 2>{}, j); break;
-          case 3: fill_v(std::integral_constant<int, 3>{}, j); break;
-          default: fill_v(std::integral_constant<int, 4>{}, j); break;
+        const float vmax = warp_max(fabsf(norm_v)), kmax = warp_max(fabsf(norm_k));
+        if (sub == 0) {
+          *reinterpret_cast<float*>(at(L::NK + slot)) = norm_k;
+          *reinterpret_cast<float*>(at(L::NV + slot)) = norm_v;
+          if (lane == 0) {
+            *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = vmax;
+            *reinterpret_cast<float*>(at(L::KMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = kmax;
+          }
         }
+        ok = ok && wait_for(c_full(j), phase(j), fail) && (j < 1 || wait_for(s_full(j - 1), phase(j - 1), fail));
+        ok = meet(7, kFill, ok);
+        if (!ok) break;
+        const bool fold = folded(c);
+        const __half2 nu = __float2half2_rn(fold ? norm_k / norm_unit(tile_max<TN>(L::KMAX, j)) : 1.f);
+        auto fill = [&](auto bits) {
+          constexpr int B = decltype(bits)::value;
+          auto turns = [&](auto scale) {
+            constexpr bool SCALE = decltype(scale)::value;
+            if constexpr (kBoxed<D, B>) {
+              const uint32_t piece = L::piece(j & 1, 0, tok / L::PR);
+#pragma unroll 1
+              for (int it = sub * L::TURNS; it < (sub + 1) * L::TURNS; ++it) {
+                uint32_t w[4];
+                read_k<D, B>(piece, tok % L::PR, it, w);
+                put_k<B, SCALE>(w, L::KT + uint32_t(it >> 1) * (TN * 128) + uint32_t(n) * 128, (it & 1) * 4, n, lane_word, nu);
+              }
+            } else {
+              put_k<B, SCALE>(kw[0], L::KT + uint32_t(n) * 128, 0, n, lane_word, nu);
+              put_k<B, SCALE>(kw[1], L::KT + uint32_t(n) * 128, 4, n, lane_word, nu);
+            }
+          };
+          if (fold) turns(std::true_type{});
+          else turns(std::false_type{});
+        };
+        switch (a.k_bits) {
+          case 1: fill(std::integral_constant<int, 1>{}); break;
+          case 2: fill(std::integral_constant<int, 2>{}); break;
+          case 3: fill(std::integral_constant<int, 3>{}); break;
+          default: fill(std::integral_constant<int, 4>{}); break;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(k_full(j));
+          mbar_arrive(c_free(j));
+        }
+        c.next(a);
+        if (c.live()) fetch();
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(v_full(j));
-        mbar_arrive(c_free(j));
+    } else {
+      // ---- V: eight tokens of one block of 64, two octets (one for d = 64)
+      constexpr int NB = TN / 64, UNITS = D == 64 ? 1 : 2;
+      const int kb = lane & 7, rest = ft >> 3;
+      const int vblock = NB == 2 ? rest >> 3 : 0, o0 = NB == 2 ? rest & 7 : rest;
+      const int v_tok = 64 * vblock + 8 * kb;
+      uint32_t vw[16];
+      auto fetch = [&] {
+        if constexpr (D == 64) {
+          if (a.v_bits & 1) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const uint8_t* vc = a.v_codes[c.s.part] + row_of(c, v_tok + ((r + kb) & 7)) * (D * a.v_bits / 8);
+              if (a.v_bits == 1) fetch_v<1>(vc, r, o0, vw);
+              else fetch_v<3>(vc, r, o0, vw);
+            }
+          }
+        }
+      };
+      if (c.live()) fetch();
+      for (int j = 0; c.live(); ++j) {
+        const bool fold = folded(c);
+        ok = ok && wait_for(c_full(j), phase(j), fail) && (!fold || wait_for(k_full(j), phase(j), fail)) &&
+             (j < 2 || wait_for(o_done(j), phase(j - 2), fail));
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        __half2 nu[4];
+        if (fold) {
+          const float inv = 1.f / norm_unit(tile_max<TN>(L::VMAX, j));
+          const uint32_t nv = L::NV + uint32_t((j & 3) * TN + v_tok) * 4;  // rows v_tok + r hold the tokens of w[r]
+          const float4 n0 = lds_f4(nv), n1 = lds_f4(nv + 16);
+          nu[0] = __floats2half2_rn(n0.x * inv, n0.y * inv), nu[1] = __floats2half2_rn(n0.z * inv, n0.w * inv);
+          nu[2] = __floats2half2_rn(n1.x * inv, n1.y * inv), nu[3] = __floats2half2_rn(n1.z * inv, n1.w * inv);
+        }
+        auto fill = [&](auto bits) {
+          constexpr int B = decltype(bits)::value;
+#pragma unroll 1
+          for (int u = 0; u < UNITS; ++u) {
+            const int o = o0 + u * (16 / NB);
+            if constexpr (kBoxed<D, B>) read_v<D, B>(L::piece(j & 1, 1, v_tok / L::PR), v_tok % L::PR, kb, o, vw);
+            const uint32_t row = L::V0 + uint32_t(j & 1) * 0x8000u + uint32_t(vblock) * (D * 128) + uint32_t(8 * o) * 128;
+            if (fold) put_v<B, true>(vw, o, row, kb, lane_word, nu);
+            else put_v<B, false>(vw, o, row, kb, lane_word, nu);
+          }
+        };
+        switch (a.v_bits) {
+          case 1: fill(std::integral_constant<int, 1>{}); break;
+          case 2: fill(std::integral_constant<int, 2>{}); break;
+          case 3: fill(std::integral_constant<int, 3>{}); break;
+          default: fill(std::integral_constant<int, 4>{}); break;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(v_full(j));
+          mbar_arrive(c_free(j));
+        }
+        c.next(a);
+        if (c.live()) fetch();
       }
-      c.next(a);
-      if (c.live()) fetch(c);
     }
   } else if (warp == kSoftWarps + kFillWarps + 1) {
     // ---------------------------------------------------------------- one thread copies the packed codes
@@ -919,8 +1072,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   }
 }
 
-template <int D, bool SPLIT> cudaError_t launch_split(const SharedArgs& a, cudaStream_t stream) {
-  auto k = shared_tc_kernel<D, SPLIT>;
+template <int D, bool SPLIT, bool FOLD> cudaError_t launch_split(const SharedArgs& a, cudaStream_t stream) {
+  auto k = shared_tc_kernel<D, SPLIT, FOLD>;
   static std::atomic<uint64_t> done;
   const cudaError_t e = allow_kernel(k, int(Tc<D>::kTotal), &done);
   if (e != cudaSuccess) return e;
@@ -947,9 +1100,10 @@ cudaError_t launch_shared_tc(const SharedArgs& a, cudaStream_t stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
   if (e != cudaSuccess) return e;
   if (uint32_t(reserved) != Tc<128>::kBase) return cudaErrorNotSupported;
-  if (a.d == 64) return a.split ? launch_split<64, true>(a, stream) : launch_split<64, false>(a, stream);
-  if (a.d == 128) return a.split ? launch_split<128, true>(a, stream) : launch_split<128, false>(a, stream);
-  return launch_split<256, false>(a, stream);
+  // bf16: what the norms lose in fp16 operands is far below a step of the output
+  if (a.d == 64) return a.split ? launch_split<64, true, false>(a, stream) : launch_split<64, false, true>(a, stream);
+  if (a.d == 128) return a.split ? launch_split<128, true, false>(a, stream) : launch_split<128, false, true>(a, stream);
+  return a.bf16 ? launch_split<256, false, true>(a, stream) : launch_split<256, false, false>(a, stream);
 }
 
 }  // namespace rrq
