@@ -42,56 +42,125 @@ template <int N> __device__ __forceinline__ void fwht_row(float (&v)[N], int lan
       }
 }
 
-// ---- queries rotated, one warp per row; block 0 also lays out the line of tiles
+// ---- the line of tiles, by one block of 256 threads.  A unit's parts are the ranges that
+// its tiles' costs fall into; part in range r of the U-th non-empty unit is segment U + r,
+// as each range before r adds at most one segment to those of the units before.
+__device__ void lay_out_unit(const SharedArgs& a, SharedSegment s, int tiles, int tokens, int unit, int units, int64_t cost,
+                             int64_t next, int tile_cost, int per, int first_part, int* count) {
+  const int r0 = int(cost / per), r1 = int((cost + int64_t(tiles - 1) * tile_cost) / per);
+  const int rn = unit + 1 < units ? int(next / per) : -1;  // the next unit's first range
+  const int token = s.token, tail = s.flags, g = s.g;
+  int at = 0;
+  for (int r = r0; r <= r1; ++r) {
+    const int end = r == r1 ? tiles : int((int64_t(r + 1) * per - cost + tile_cost - 1) / tile_cost);
+    s.token = token + at * a.tile;
+    s.tokens = (end * a.tile < tokens ? end * a.tile : tokens) - at * a.tile;
+    s.tiles = end - at;
+    s.state = (first_part + r - r0) * a.hkv + g;
+    s.flags = tail | (r < r1 || rn != r ? 2 : 0);
+    a.segs[2 * (unit + r)] = make_int4(s.token, s.tokens, s.tiles, s.g);
+    a.segs[2 * (unit + r) + 1] = make_int4(s.row0, s.nrows, s.state, s.flags);
+    if (r > r0 || unit == 0) a.begin[r] = unit + r;
+    at = end;
+  }
+  if (rn > r1) a.begin[rn] = unit + 1 + rn;
+  *count = r1 - r0 + 1;
+}
+
+__device__ void lay_out(const SharedArgs& a) {
+  __shared__ int2 s_sum[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int r = tid; r < a.grid; r += 256) a.begin[r] = -1;
+  // tokens and tiles of a sequence's tail
+  auto length = [&](int64_t b) {
+    if (b >= a.batch || a.lens == nullptr) return 0;
+    const int n = a.lens[b];
+    return n < 0 ? 0 : n > a.cap ? int(a.cap) : n;
+  };
+  // all tails' tiles and how many are not empty
+  int tiles = 0, filled = 0;
+  for (int64_t b = tid; b < a.batch; b += 256) {
+    const int n = (length(b) + a.tile - 1) / a.tile;
+    tiles += n;
+    filled += n > 0;
+  }
+  tiles = __reduce_add_sync(kFull, tiles);
+  filled = __reduce_add_sync(kFull, filled);
+  if (lane == 0) s_sum[warp] = make_int2(tiles, filled);
+  __syncthreads();
+  tiles = filled = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) tiles += s_sum[w].x, filled += s_sum[w].y;
+  const int64_t pcost = int64_t(a.units_p) * a.ptiles * a.pcost;
+  const int64_t cost = pcost + int64_t(a.hkv) * (int64_t(tiles) * a.tcost + int64_t(filled) * a.scost);
+  const int64_t even = (cost + a.grid - 1) / a.grid;
+  const int per = int(even < a.min_cost ? a.min_cost : even);
+  const int units = a.units_p + a.hkv * filled;
+  for (int u = tid; u < a.units_p; u += 256) {
+    SharedSegment s = {};
+    s.g = u / a.row_tiles;
+    s.row0 = (u % a.row_tiles) * 128;
+    s.nrows = int(a.rows - s.row0 < 128 ? a.rows - s.row0 : 128);
+    const int64_t at = int64_t(u) * a.ptiles * a.pcost;
+    lay_out_unit(a, s, a.ptiles, int(a.prefix), u, units, at, at + int64_t(a.ptiles) * a.pcost, a.pcost, per, 0, a.counts + u);
+  }
+  int before = 0, some_before = 0;
+  for (int64_t b0 = 0; b0 < a.batch && a.cap > 0; b0 += 256) {
+    const int64_t b = b0 + tid;
+    const int len = length(b), mine = (len + a.tile - 1) / a.tile;
+    int sum = mine, some = mine > 0;  // inclusive prefixes: of the warp, then of the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, sum, o), y = __shfl_up_sync(kFull, some, o);
+      if (lane >= o) sum += x, some += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = make_int2(sum, some);
+    __syncthreads();
+    int all = 0, all_some = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const int2 x = s_sum[w];
+      if (w < warp) sum += x.x, some += x.y;
+      all += x.x;
+      all_some += x.y;
+    }
+    const int tiles_before = before + sum - mine, units_before = some_before + some - (mine > 0);
+    before += all;
+    some_before += all_some;
+    if (b >= a.batch) continue;
+    for (int g = 0; g < a.hkv; ++g) {
+      int* count = a.counts + a.units_p + b * a.hkv + g;
+      if (mine == 0) {
+        *count = 0;
+        continue;
+      }
+      SharedSegment s = {};
+      s.token = int(b * a.cap);
+      s.g = g;
+      s.row0 = int(b * a.group);
+      s.nrows = a.group;
+      s.flags = 1;
+      const int64_t at = pcost + (int64_t(a.hkv) * tiles_before + int64_t(g) * mine) * a.tcost +
+                         (int64_t(a.hkv) * units_before + g) * a.scost;
+      lay_out_unit(a, s, mine, len, a.units_p + a.hkv * units_before + g, units, at, at + int64_t(mine) * a.tcost + a.scost, a.tcost,
+                   per, a.parts_p, count);
+    }
+  }
+}
+
+// ---- queries rotated, one warp per row; one block more lays out the line of tiles
 template <int D>
 __global__ void __launch_bounds__(256) shared_prepare_kernel(const SharedArgs a) {
   constexpr int N = D / 32;
-  __shared__ int2 s_sum[8];
   pdl_release();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x == 0) {
-    int before = 0, filled = 0;
-    for (int64_t b0 = 0; b0 < a.batch; b0 += 256) {
-      const int64_t b = b0 + tid;
-      int len = 0;
-      if (b < a.batch && a.lens) {
-        const int n = a.lens[b];
-        len = n < 0 ? 0 : n > a.cap ? int(a.cap) : n;
-      }
-      const int mine = (len + a.tile - 1) / a.tile;
-      int sum = mine, some = mine > 0;  // inclusive prefixes: of the warp, then of the block
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(kFull, sum, o), y = __shfl_up_sync(kFull, some, o);
-        if (lane >= o) sum += x, some += y;
-      }
-      if (lane == 31) s_sum[warp] = make_int2(sum, some);
-      __syncthreads();
-      int all = 0, all_some = 0;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const int2 x = s_sum[w];
-        if (w < warp) sum += x.x, some += x.y;
-        all += x.x;
-        all_some += x.y;
-      }
-      if (b < a.batch) a.tails[b] = make_int4(before + sum - mine, filled + some - (mine > 0), len, mine);
-      before += all;
-      filled += all_some;
-      __syncthreads();
-    }
-    if (tid == 0) {
-      a.tails[a.batch] = make_int4(before, filled, 0, 0);
-      const int total = a.hkv * (a.row_tiles * a.ptiles + before);
-      const int64_t cost = int64_t(a.hkv) * (int64_t(a.row_tiles) * a.ptiles * a.pcost + int64_t(before) * a.tcost +
-                                             int64_t(filled) * a.scost);
-      const int per = int((cost + a.grid - 1) / a.grid);
-      a.head[0] = total;
-      a.head[1] = per < a.min_cost ? a.min_cost : per;
-    }
+    lay_out(a);
+    return;
   }
-  const int64_t row = int64_t(blockIdx.x) * 8 + warp;  // b·hq + h
+  const int64_t row = int64_t(blockIdx.x - 1) * 8 + warp;  // b·hq + h
   if (row >= a.batch * a.hq) return;
   float v[N];
 #pragma unroll
@@ -146,18 +215,17 @@ __global__ void __launch_bounds__(256) shared_partial_kernel(const SharedArgs a)
   if (tid < 16) s_lev[tid] = a.k_levels[tid];
   else if (tid < 32) s_lev[tid] = a.v_levels[tid - 16];
   const int range = blockIdx.x;
-  int pos, end;
-  range_tiles(a, range, &pos, &end);
-  while (pos < end) {
-    const Segment s = segment_at(a, range, pos, end);
-    pos += s.tiles;
-    const int kv = s.part;
+  for (int i = a.begin[range]; i >= 0;) {
+    const SharedSegment s = shared_segment(a, i);
+    i = s.flags & 2 ? -1 : i + 1;
+    const int kv = s.flags & 1;
+    const int64_t state = int64_t(s.state) * a.rows + s.row0;
     // 32 tokens' values (codes' levels, unscaled) into s_kv; tokens past the end repeat the last
     auto load = [&](const uint8_t* codes, int bits, const float* lev, int64_t t) {
       for (int i = tid; i < 32 * (D / 8); i += 256) {
         const int tok = i / (D / 8), o = i % (D / 8);
-        const int64_t tt = t + tok < s.t1 ? t + tok : s.t1 - 1;
-        const uint8_t* p = codes + ((s.token_base + tt) * a.hkv + s.g) * (D * bits / 8) + o * bits;
+        const int64_t tt = t + tok < s.tokens ? t + tok : s.tokens - 1;
+        const uint8_t* p = codes + ((s.token + tt) * a.hkv + s.g) * (D * bits / 8) + o * bits;
         uint32_t w = 0;
         for (int k = 0; k < bits; ++k) w |= uint32_t(p[k]) << (8 * k);
         w = octet_nibbles(w, bits);
@@ -171,12 +239,12 @@ __global__ void __launch_bounds__(256) shared_partial_kernel(const SharedArgs a)
       for (int i = lane; i < D; i += 32) s_q[warp * D + i] = q[i];
       float m = -INFINITY, l = 0.f, acc[N];
       for (int i = 0; i < N; ++i) acc[i] = 0.f;
-      for (int64_t t = s.t0; t < s.t1; t += 32) {
+      for (int64_t t = 0; t < s.tokens; t += 32) {
         __syncthreads();
         load(a.k_codes[kv], a.k_bits, s_lev, t);
         __syncthreads();
-        const bool valid = t + lane < s.t1;
-        const int64_t row = (s.token_base + (valid ? t + lane : s.t1 - 1)) * a.hkv + s.g;
+        const bool valid = t + lane < s.tokens;
+        const int64_t row = (s.token + (valid ? t + lane : s.tokens - 1)) * a.hkv + s.g;
         float x = 0.f;
         for (int i = 0; i < D; ++i) x = fmaf(s_q[warp * D + i], s_kv[lane * P + i], x);
         x = valid ? x * a.k_norms[kv][row] : -INFINITY;
@@ -199,8 +267,8 @@ __global__ void __launch_bounds__(256) shared_partial_kernel(const SharedArgs a)
       }
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
       if (live) {
-        if (lane == 0) a.stats[s.state + r] = make_float2(m, l);
-        for (int i = 0; i < N; ++i) a.acc[(s.state + r) * D + 32 * i + lane] = acc[i];
+        if (lane == 0) a.stats[state + r] = make_float2(m, l);
+        for (int i = 0; i < N; ++i) a.acc[(state + r) * D + 32 * i + lane] = acc[i];
       }
       __syncthreads();
     }
@@ -219,16 +287,9 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
   const int64_t b = row / a.hq;
   const int h = int(row % a.hq), g = h / a.group;
   const int64_t r = b * a.group + h % a.group;
-  int np = 0, nt = 0;  // parts of the prefix, of the tail
-  if (a.ptiles > 0) {
-    const int first = (g * a.row_tiles + int(r / 128)) * a.ptiles;
-    np = range_of_cost(a, int64_t(first + a.ptiles - 1) * a.pcost) - range_of_cost(a, int64_t(first) * a.pcost) + 1;
-  }
-  const int4 tail = a.tails[b];
-  if (tail.w > 0) {
-    const int64_t first = tail_cost(a, tail, g);
-    nt = range_of_cost(a, first + int64_t(tail.w - 1) * a.tcost) - range_of_cost(a, first) + 1;
-  }
+  // parts of the prefix, of the tail
+  const int np = a.units_p > 0 ? a.counts[g * a.row_tiles + int(r / 128)] : 0;
+  const int nt = a.cap > 0 ? a.counts[a.units_p + b * a.hkv + g] : 0;
   auto state = [&](int i) {
     const int p = i < np ? i : a.parts_p + (i - np);
     return (int64_t(p) * a.hkv + g) * a.rows + r;
@@ -267,7 +328,7 @@ int sm_count() {
 template <int D> cudaError_t launch_d(const SharedArgs& a, cudaStream_t stream) {
   const int64_t rows = a.batch * a.hq;
   const dim3 blocks(unsigned((rows + 7) / 8));
-  cudaError_t e = launch_pdl(shared_prepare_kernel<D>, blocks, dim3(256), 0, stream, a);
+  cudaError_t e = launch_pdl(shared_prepare_kernel<D>, dim3(blocks.x + 1), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
   if constexpr (D > kTcMaxD) {
     constexpr size_t smem = (32 * (D + 1) + 8 * D + 32) * 4;
@@ -300,6 +361,7 @@ bool attention_shared_plan(SharedArgs* a) {
   if (tunits == 0) return true;  // no sequence: nothing runs
   if (pt > most / punits || tt > most / tunits || (punits * pt + tunits * (tt + 1)) >= most / 10) return false;
   a->ptiles = int(pt);
+  a->units_p = pt > 0 ? int(punits) : 0;
   a->grid = sm_count();
   // costs, measured: a tile against up to 16 rows 1.7 us, against more 2.5 us, a tail's start
   // and end 2 us
@@ -338,12 +400,15 @@ void attention_shared_levels(SharedArgs* a, bool default_k, bool default_v) {
 
 size_t attention_shared_layout(SharedArgs* a, void* base) {
   const size_t rows = size_t(a->rows) * size_t(a->hkv), parts = size_t(a->parts_p) + size_t(a->parts_t);
-  const size_t head = pad256(256 + (size_t(a->batch) + 1) * 16);
+  const size_t units = size_t(a->units_p) + (a->cap > 0 ? size_t(a->batch) * a->hkv : 0);
+  const size_t begin = pad256(size_t(a->grid) * 4), counts = pad256(units * 4), segs = pad256((units + a->grid) * 32);
+  const size_t head = begin + counts + segs;
   const size_t q = pad256(rows * a->d * 4), qe = pad256(rows * 4), st = pad256(parts * rows * 8);
   uint8_t* p = static_cast<uint8_t*>(base);
   if (p != nullptr) {
-    a->head = reinterpret_cast<int*>(p);
-    a->tails = reinterpret_cast<int4*>(p + 256);
+    a->begin = reinterpret_cast<int*>(p);
+    a->counts = reinterpret_cast<int*>(p + begin);
+    a->segs = reinterpret_cast<int4*>(p + begin + counts);
     a->qrot = reinterpret_cast<float*>(p + head);
     a->qh = reinterpret_cast<__half*>(p + head);
     a->ql = a->qh + rows * a->d;

@@ -37,6 +37,7 @@ struct SharedArgs {
   int pcost, tcost;      // cost of a tile of the prefix, of a tail
   int scost;             // of a tail besides its tiles
   int min_cost;          // of a range
+  int units_p;           // prefix units: hkv · row_tiles, or 0 without a prefix
   int parts_p, parts_t;  // most ranges that share a prefix unit, a tail unit
   int k_bits, v_bits;
   uint64_t k_seed, v_seed;
@@ -48,8 +49,9 @@ struct SharedArgs {
   float k_alpha, v_alpha;
   int split;             // queries as two fp16 parts
   // workspace
-  int* head;      // [0] tiles in all, [1] cost per range
-  int4* tails;    // entry b: tiles and non-empty tails before b (of one kv head), tokens, tiles; one more behind the last
+  int* begin;     // [grid] a range's first segment, −1 for a range without tiles
+  int* counts;    // [units] parts of every unit: prefix units (g · row_tiles + rt), then tails (b · hkv + g)
+  int4* segs;     // two words per segment, those of a range one after the other (SharedSegment)
   float* qrot;    // rotated queries, row (g·rows + r), d values (d = 512), or in their place
   __half* qh;     //   the same as fp16 times a power of two per row,
   __half* ql;     //   what that rounding left, when split,

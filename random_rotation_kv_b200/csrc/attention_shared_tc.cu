@@ -328,66 +328,25 @@ __device__ __forceinline__ void mask(float2 (&y)[16], int h, int valid, float v)
   }
 }
 
-// Finding a place in the line takes searches and 64-bit divisions; out of line, as five
-// roles do it once, and the tiles' code has to stay in the instruction cache.
-__device__ __noinline__ void find_segment(const SharedArgs& a, int range, int pos, int end, Segment* s) {
-  *s = segment_at(a, range, pos, end);
-}
-__device__ __noinline__ void find_range(const SharedArgs& a, int range, int* pos, int* end) {
-  range_tiles(a, range, pos, end);
-}
-
-// Position in a range, one tile at a time.  The segments after the first begin with their
-// unit, so they follow without a search (but for tails of length 0); the next tail's
-// entry is read one sequence ahead.
+// Position in a range's segments, one tile at a time.
 struct Cursor {
-  int range, pos, end, i;
-  int4 ahead;  // entry of the sequence after this tail's
-  Segment s;
-  __device__ __forceinline__ Cursor(const SharedArgs& a, int r) : range(r), i(0) {
-    int p, e;
-    find_range(a, r, &p, &e);
-    pos = p;
-    end = e;
-    if (pos < end) seek(a);
+  int index, i;  // the segment (−1 at the end), the tile in it
+  SharedSegment s;
+  __device__ __forceinline__ Cursor(const SharedArgs& a, int range) : index(a.begin[range]), i(0) {
+    if (index >= 0) load(a);
   }
-  __device__ __forceinline__ void seek(const SharedArgs& a) {
-    Segment t;
-    find_segment(a, range, pos, end, &t);
-    s = t;
-    entry = a.tails[s.part ? s.b : 0];
-    ahead = a.tails[s.part ? s.b + 1 : 0];
+  __device__ __forceinline__ void load(const SharedArgs& a) {
+    s = shared_segment(a, index);
+    if (!(s.flags & 2)) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.segs + 2 * (index + 1)));
   }
-  int4 entry;  // of this tail's sequence
-  __device__ __forceinline__ bool live() const { return pos < end; }
-  __device__ __forceinline__ void next(const SharedArgs& a) {
-    if (++i < s.tiles) return;
-    pos += s.tiles;
+  __device__ __forceinline__ bool live() const { return index >= 0; }
+  __device__ __forceinline__ void next_segment(const SharedArgs& a) {
     i = 0;
-    if (pos >= end) return;
-    if (s.part == 0) {
-      const int rt = s.b + 1 < a.row_tiles ? s.b + 1 : 0, g = s.g + (rt == 0);
-      if (g == a.hkv) {
-        seek(a);
-        return;
-      }
-      prefix_unit(a, g, rt, &s);
-      cut_segment(a, 0, a.ptiles, a.prefix, end - pos, 0, &s);
-    } else {
-      int g = s.g + 1;
-      int64_t b = s.b;
-      if (g == a.hkv) {
-        if (ahead.w == 0) {
-          seek(a);
-          return;
-        }
-        g = 0;
-        entry = ahead;
-        ahead = a.tails[++b + 1];
-      }
-      tail_unit(a, g, b, &s);
-      cut_segment(a, 0, entry.w, entry.z, end - pos, 0, &s);
-    }
+    index = s.flags & 2 ? -1 : index + 1;
+    if (index >= 0) load(a);
+  }
+  __device__ __forceinline__ void next(const SharedArgs& a) {
+    if (++i == s.tiles) next_segment(a);
   }
 };
 
@@ -455,33 +414,47 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     Cursor c(a, range);
     int j = 0, seg = 0;
     bool staged = false;  // the segment's queries are in shared memory already
-    // few rows: the queries of a segment as an operand, rows past its own as zeros
-    auto stage = [&](const Segment& s, int number) {
+    // few rows: the queries of a segment as an operand, rows past its own as zeros; read from
+    // global memory a segment before they are staged
+    uint4 qv[SPLIT ? 2 : 1];
+    float qe = 1.f;
+    const int q_row = (tid >> 3) & 15, q_chunk = (tid & 7) + ((tid >> 7) << 3);  // row, chunk of 8 coordinates
+    auto read_queries = [&](const SharedSegment& s) {
       const int64_t qrow = int64_t(s.g) * a.rows + s.row0;
-      const int r = (tid >> 3) & 15, k0 = (tid & 7) + ((tid >> 7) << 3);  // row, chunk of 8 coordinates
+      if (q_row < s.nrows && q_chunk < D / 8) {
 #pragma unroll
-      for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
-        if (k0 < D / 8) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (r < s.nrows) v = __ldcg(reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + (qrow + r) * D) + k0);
-          sts_v4(L::QB + uint32_t(part * (D / 64) + (k0 >> 3)) * 2048 + uint32_t(r) * 128 + (uint32_t((k0 ^ r) & 7) << 4), v.x, v.y,
-                 v.z, v.w);
+        for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+          qv[part] = __ldcg(reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + (qrow + q_row) * D) + q_chunk);
+      }
+      if (tid < 16 && tid < s.nrows) qe = __ldcg(a.qexp + qrow + tid);
+    };
+    auto stage = [&](const SharedSegment& s, int number) {
+      if (q_chunk < D / 8) {
+#pragma unroll
+        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+          const uint4 v = q_row < s.nrows ? qv[part] : make_uint4(0, 0, 0, 0);
+          sts_v4(L::QB + uint32_t(part * (D / 64) + (q_chunk >> 3)) * 2048 + uint32_t(q_row) * 128 +
+                     (uint32_t((q_chunk ^ q_row) & 7) << 4), v.x, v.y, v.z, v.w);
         }
-      if (tid < 16)
-        *reinterpret_cast<float*>(at(L::RS + uint32_t(number & 1) * 64 + uint32_t(tid) * 4)) = tid < s.nrows ? __ldcg(a.qexp + qrow + tid) : 1.f;
+      }
+      if (tid < 16) *reinterpret_cast<float*>(at(L::RS + uint32_t(number & 1) * 64 + uint32_t(tid) * 4)) = tid < s.nrows ? qe : 1.f;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     };
     while (c.live()) {
-      const Segment& s = c.s;
+      const SharedSegment s = c.s;
       bool ok = *fail == 0;
       if (D <= 128 && s.nrows <= kFewRows) {
         if constexpr (D <= 128) {
           // ---- few rows: lane = token, columns = rows; this half's rows [8·half, + 8)
           const bool mine = 8 * half < s.nrows;
-          if (!staged) stage(s, seg);
+          if (!staged) {
+            read_queries(s);
+            stage(s, seg);
+          }
           staged = false;
+          if (!(s.flags & 2)) read_queries(shared_segment(a, c.index + 1));
           float rs[8], m[8], mp[8], l[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r) m[r] = mp[r] = l[r] = 0.f;
@@ -491,8 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             ok = __all_sync(kFull, ok);
             tc_fence_after();
             if (mine) {
-              const int64_t left = s.t1 - s.t0 - int64_t(i) * TN;
-              const bool live = token_of(ln) < left;
+              const bool live = token_of(ln) < s.tokens - i * TN;
               const uint32_t wm = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(half) * 128;
               float y[8], nv = 0.f;
               if (ok) {
@@ -578,10 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           }
           // the next segment's queries go in while this one's last product runs: S of all its
           // tiles is done
-          const Segment done = s;
-          c.i = s.tiles - 1;
-          c.next(a);
-          if (c.live() && c.s.nrows <= kFewRows) {
+          c.next_segment(a);
+          if (c.live()) {  // tails behind a prefix of few rows have no more rows than it
             stage(c.s, seg + 1);
             staged = true;
           }
@@ -600,14 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               sts_v4(wl + uint32_t(quarter) * 32 + 16, __float_as_uint(l[4]), __float_as_uint(l[5]), __float_as_uint(l[6]), __float_as_uint(l[7]));
             }
             ok = meet(uint32_t(5 + half), 128, ok);
-            if (quarter == 0 && lane < 8 && 8 * half + lane < done.nrows) {
+            if (quarter == 0 && lane < 8 && 8 * half + lane < s.nrows) {
               float sum = 0.f, mine_mp = mp[0];
 #pragma unroll
               for (int q = 0; q < 4; ++q) sum += __uint_as_float(lds_code(wl + uint32_t(q) * 32 + uint32_t(lane) * 4, 4));
 #pragma unroll
               for (int r = 1; r < 8; ++r)
                 if (lane == r) mine_mp = mp[r];
-              a.stats[done.state + 8 * half + lane] = ok ? make_float2(mine_mp, sum) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
+              a.stats[int64_t(s.state) * a.rows + s.row0 + 8 * half + lane] = ok ? make_float2(mine_mp, sum) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
             }
             if (ok) {
               uint32_t o[8];
@@ -615,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               tmem_ld_wait();
 #pragma unroll
               for (int r = 0; r < 8; ++r)
-                if (8 * half + r < done.nrows && ln < D) a.acc[(done.state + 8 * half + r) * D + ln] = __uint_as_float(o[r]);
+                if (8 * half + r < s.nrows && ln < D)
+                  a.acc[(int64_t(s.state) * a.rows + s.row0 + 8 * half + r) * D + ln] = __uint_as_float(o[r]);
             }
             // the next segment writes this slot of the exchange again
             meet(uint32_t(5 + half), 128, true);
@@ -657,8 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           ok = __all_sync(kFull, ok);
           tc_fence_after();
           if (warp_ok) {
-            const int64_t left = s.t1 - s.t0 - int64_t(i) * TN;
-            const int valid = int(left < TN ? left : TN);
+            const int left = s.tokens - i * TN, valid = left < TN ? left : TN;
             const bool full = valid == TN;
             const uint32_t sb = tl + uint32_t(L::S + (j & 1) * TN + half * TH);
             const uint32_t nk = L::NK + uint32_t((j & 3) * TN + half * TH) * 4, nv = L::NV + uint32_t((j & 3) * TN + half * TH) * 4;
@@ -789,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           const uint32_t xch = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(ln) * 4;
           if (half) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch), "f"(l) : "memory");
           ok = meet(pair, 64, ok);
-          const int64_t st = s.state + ln;
+          const int64_t st = int64_t(s.state) * a.rows + s.row0 + ln;
           if (!half && row_ok)
             a.stats[st] = ok ? make_float2(mp, l + __uint_as_float(lds_code(xch, 4))) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
           if (ok) {
@@ -810,8 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           }
           meet(pair, 64, true);  // the next segment writes this slot of the exchange again
         }
-        c.i = s.tiles - 1;
-        c.next(a);
+        c.next_segment(a);
       }
       ++seg;
     }
@@ -822,8 +791,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const uint32_t lane_word = L::TABLE | uint32_t(lane * 4) | (v_side ? 128u : 0u);
     // row of the cache of a tile's token t; rows past the segment's end repeat its last
     auto row_of = [&](const Cursor& c, int t) {
-      const int64_t tt = c.s.t0 + int64_t(c.i) * TN + t;
-      return (c.s.token_base + (tt < c.s.t1 ? tt : c.s.t1 - 1)) * a.hkv + c.s.g;
+      const int tt = c.i * TN + t;
+      return int64_t(c.s.token + (tt < c.s.tokens ? tt : c.s.tokens - 1)) * a.hkv + c.s.g;
     };
     auto folded = [&](const Cursor& c) { return FOLD && !(D <= 128 && c.s.nrows <= kFewRows); };
     Cursor c(a, range);
@@ -836,10 +805,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       float norm_k = 0.f, norm_v = 0.f;
       auto fetch = [&] {  // what comes from global memory for the cursor's tile
         const int64_t row = row_of(c, tok);
-        norm_k = __ldg(a.k_norms[c.s.part] + row);
-        norm_v = c.s.t0 + int64_t(c.i) * TN + tok < c.s.t1 ? __ldg(a.v_norms[c.s.part] + row) : 0.f;
+        norm_k = __ldg(a.k_norms[c.s.flags & 1] + row);
+        norm_v = c.i * TN + tok < c.s.tokens ? __ldg(a.v_norms[c.s.flags & 1] + row) : 0.f;
         if constexpr (D == 64) {
-          const uint8_t* kc = a.k_codes[c.s.part] + row * (D * a.k_bits / 8);
+          const uint8_t* kc = a.k_codes[c.s.flags & 1] + row * (D * a.k_bits / 8);
           if (a.k_bits & 1) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -915,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           if (a.v_bits & 1) {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-              const uint8_t* vc = a.v_codes[c.s.part] + row_of(c, v_tok + ((r + kb) & 7)) * (D * a.v_bits / 8);
+              const uint8_t* vc = a.v_codes[c.s.flags & 1] + row_of(c, v_tok + ((r + kb) & 7)) * (D * a.v_bits / 8);
               if (a.v_bits == 1) fetch_v<1>(vc, r, o0, vw);
               else fetch_v<3>(vc, r, o0, vw);
             }
@@ -977,12 +946,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         if (!ok) break;
         const uint32_t bar = smem_addr(c_full(j));
         mbarrier_expect_tx(bar, bytes);
-        const int64_t t = c.s.token_base + c.s.t0 + int64_t(c.i) * TN;
+        const int t = c.s.token + c.i * TN, part = c.s.flags & 1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t y = t + h * L::PR;  // rows past the cache's end are filled with zeros
-          if (kbox) tma_load_2d(L::piece(j & 1, 0, h), &maps.k[c.s.part], c.s.g * krow, int(y), bar);
-          if (vbox) tma_load_2d(L::piece(j & 1, 1, h), &maps.v[c.s.part], c.s.g * vrow, int(y), bar);
+          const int y = t + h * L::PR;  // rows past the cache's end are filled with zeros
+          if (kbox) tma_load_2d(L::piece(j & 1, 0, h), &maps.k[part], c.s.g * krow, y, bar);
+          if (vbox) tma_load_2d(L::piece(j & 1, 1, h), &maps.v[part], c.s.g * vrow, y, bar);
         }
       }
       // copies still in flight end before the CTA does
@@ -1050,8 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         __syncwarp();
       }
       ++seg;
-      c.i = tiles - 1;
-      c.next(a);
+      c.next_segment(a);
     }
     // products still in flight end before the tensor memory is given up
     uint64_t* drain = &bars[11];
