@@ -22,13 +22,14 @@
 //  * warp 17 copies the packed codes of two tiles ahead into shared memory (TMA boxes of
 //    half a tile's rows, swizzled where rows are 32, 64 or 128 bytes; rows of 8 and 24 bytes
 //    are not multiples of TMA's 16 and are read by the filling warps themselves);
-//  * warps 8–15 turn code pairs into level pairs by one shared-memory lookup per byte
-//    (tables of 256 pairs, one copy per lane so that no bank conflicts; a value byte holds
-//    one coordinate of two tokens, so V is laid out transposed without a transposition)
-//    and write K [token][coordinate] and V [coordinate][token] as fp16 in the 128-byte
-//    swizzle, V in two stages.  Row 8k + e of a tile's 64 is token 8k + (e + k) mod 8:
-//    the eight lanes that share a wavefront then read eight neighbouring code rows and
-//    write eight different chunks, for K and V alike;
+//  * warps 8–11 and 12–15 turn K and V codes into fp16 levels, one token per thread, by one
+//    shared-memory lookup per byte of two coordinates (tables of 256 pairs, one copy per lane
+//    so that no bank conflicts), and write rows [token][coordinate] in the 128-byte swizzle,
+//    V in two stages: as they lie, K is a K-major operand and V, whose tokens are summed over,
+//    an MN-major one.  Row 8k + e of a tile's 64 is token 8k + (e + k) mod 8, so the eight
+//    lanes that share a wavefront read eight neighbouring code rows.  For bf16 queries the
+//    norms (over their tile's unit) are multiplied in here, and for more than 16 rows they
+//    are out of the weights' way;
 //  * warp 16 issues the products; the next tile's S runs while this tile's weights are made;
 //  * warps 0–7 make the weights: two threads per query row with half of the tokens each,
 //    the row's maximum met through shared memory, weights back into S's own columns as
@@ -53,7 +54,7 @@ constexpr int kThreads = (kSoftWarps + kFillWarps + 2) * 32;
 
 template <int D> struct Tc {
   static constexpr int TN = D <= 128 ? 128 : 64;     // tokens per tile
-  static constexpr int TURNS = D / 32 * TN / kFill;  // K: turns of 4 octets per thread (a token's, or half a token's)
+  static constexpr int TURNS = D / 32 * TN / kFill;  // turns of 4 octets per filling thread (a token's, or half a token's)
   static constexpr int PR = TN / 2;                  // rows of a piece of packed codes
   static constexpr uint32_t TILE = TN * D * 2;       // bytes of a K or V stage
   // shared addresses (the dynamic base is checked to be kBase)
@@ -63,19 +64,23 @@ template <int D> struct Tc {
   static constexpr uint32_t FAIL = 0x4D0;
   static constexpr uint32_t VMAX = 0x500;            // [4 tiles][4 warps] largest value norm
   static constexpr uint32_t KMAX = 0x540;            // and key norm
+  static constexpr uint32_t VOWN = 0x600;            // the same as VMAX, for the V-filling warps alone
   static constexpr uint32_t NK = 0x800, NV = 0x1000; // [4 tiles][TN] norms
   static constexpr uint32_t PT = 0x2000;             // few rows: weights [2 tiles][2 × 64 tokens][16 rows], swizzled
   static constexpr uint32_t QB = 0x4000;             // few rows: queries [part][64 coordinates][16 rows], swizzled
   static constexpr uint32_t RS = 0x580;              // few rows: [2 segments][16] powers of two taken out of the queries
   static constexpr uint32_t XCH = 0x6000;            // [2 tiles][2 halves][128 rows] maxima
   // packed codes: eight 4 KB pieces of half a tile's rows, at most 64 (d = 256: 128) bytes each
-  static constexpr uint32_t piece(int stage, int v, int half) { return 0x8000u + uint32_t(stage * 4 + v * 2 + half) * 0x1000u; }
+  __host__ __device__ static constexpr uint32_t piece(int stage, int v, int half) {
+    return 0x8000u + uint32_t(stage * 4 + v * 2 + half) * 0x1000u;
+  }
   static constexpr uint32_t TABLE = 0x10000;         // K pairs at +0, V pairs at +128 of every 256 bytes
   static constexpr uint32_t KT = 0x20000;            // K tile
   static constexpr uint32_t V0 = 0x28000;            // V stages
   static constexpr size_t kTotal = 0x38000 - kBase;
   // tensor memory columns
   static constexpr int S = 0, O = 2 * TN, Q = O + D, QL = Q + D / 2;
+  // fp16 operands, fp32 sums, M = 128; bits 15 and 16: A, B MN-major
   static constexpr uint32_t idesc(int n) { return (1u << 4) | (uint32_t(n / 8) << 17) | ((128u / 16) << 24); }
   static_assert(NV + 4 * TN * 4 <= PT && TILE <= 0x8000 && kTotal <= 227 * 1024, "layout");
 };
@@ -101,6 +106,18 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle: rows of 64 MN
+// elements, one per K index, eight rows to a 1024-byte group; `block`: bytes from one run
+// of 64 MN elements to the next.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr, uint32_t block) {
+  uint64_t d = 0;
+  d |= uint64_t((saddr >> 4) & 0x3FFFu);
+  d |= uint64_t((block >> 4) & 0x3FFFu) << 16;  // leading offset: along MN
+  d |= uint64_t(1024u >> 4) << 32;              // stride offset: along K
+  d |= uint64_t(1) << 46;                       // descriptor version for sm_100
+  d |= uint64_t(2) << 61;                       // layout: 128-byte swizzle
+  return d;
 }
 // D[tmem] (+)= A[tmem]·B, kind::f16, one CTA.
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -204,8 +221,8 @@ __device__ __forceinline__ uint32_t lds_code(uint32_t addr, int bytes) {
 }
 
 // ---- the filling warps' reads, by code width
-// Four octets (B words) of a K row, number `it`: from a piece (row r), or from global memory.
-template <int D, int B> __device__ __forceinline__ void read_k(uint32_t piece, int r, int it, uint32_t (&w)[4]) {
+// Four octets (B words) of a code row, number `it`, from a piece (row r).
+template <int D, int B> __device__ __forceinline__ void read_octets(uint32_t piece, int r, int it, uint32_t (&w)[4]) {
   constexpr int PITCH = D * B / 8;
   const uint32_t off = uint32_t(it) * (4 * B);
   if constexpr (B == 4) {
@@ -227,31 +244,6 @@ template <int B> __device__ __forceinline__ uint32_t octet_of(const uint32_t (&w
   if (sh + 8 * B > 32) v = __funnelshift_r(w[k], w[k + 1 < 4 ? k + 1 : 3], sh);
   return octet_nibbles(v & (B == 3 ? 0xffffffu : B == 2 ? 0xffffu : 0xffu), B);
 }
-// The B bytes of octet o of the 8 tokens of block kb, token 8·kb + (r + kb) mod 8 in w[r]
-// (3-bit octets as the two words they may touch).
-template <int D, int B>
-__device__ __forceinline__ void read_v(uint32_t piece, int row0, int kb, int o, uint32_t (&w)[16]) {
-  constexpr int PITCH = D * B / 8;
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int row = row0 + ((r + kb) & 7);
-    if constexpr (B == 3) {
-      w[r] = lds_code(piece + code_at<PITCH>(row, uint32_t((3 * o) / 4 * 4)), 4);
-      w[8 + r] = lds_code(piece + code_at<PITCH>(row, uint32_t((3 * o + 2) / 4 * 4)), 4);
-    } else {
-      w[r] = lds_code(piece + code_at<PITCH>(row, uint32_t(o * B)), B);
-    }
-  }
-}
-template <int B> __device__ __forceinline__ void fetch_v(const uint8_t* p, int r, int o, uint32_t (&w)[16]) {
-  if constexpr (B == 3) {
-    w[r] = __ldg(reinterpret_cast<const uint32_t*>(p) + (3 * o) / 4);
-    w[8 + r] = __ldg(reinterpret_cast<const uint32_t*>(p) + (3 * o + 2) / 4);
-  } else {
-    w[r] = __ldg(p + o);  // one-bit octets
-  }
-}
-
 template <bool SCALE> __device__ __forceinline__ uint32_t times(uint32_t pair, __half2 nu) {
   if constexpr (!SCALE) return pair;
   const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&pair), nu);
@@ -267,10 +259,10 @@ template <int K> __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_
   return lds_u32(__byte_perm(w, lane_word, K == 0 ? 0x7604u : K == 1 ? 0x7614u : K == 2 ? 0x7624u : 0x7634u));
 }
 
-// Four octets of a token's K row, chunks c0 .. c0 + 3 of `row`; SCALE: times `nu`.  All
+// Four octets of a token's row as levels, chunks c0 .. c0 + 3 of `row`; SCALE: times `nu`.  All
 // lookups come before the first store: a load is not moved ahead of a store that might alias it.
 template <int B, bool SCALE>
-__device__ __forceinline__ void put_k(const uint32_t (&w)[4], uint32_t row, int c0, int n, uint32_t lane_word, __half2 nu) {
+__device__ __forceinline__ void put_octets(const uint32_t (&w)[4], uint32_t row, int c0, int n, uint32_t lane_word, __half2 nu) {
   uint32_t p[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -282,40 +274,6 @@ __device__ __forceinline__ void put_k(const uint32_t (&w)[4], uint32_t row, int 
   for (int i = 0; i < 4; ++i)
     sts_v4(row + (uint32_t((c0 + i) ^ (n & 7)) << 4), times<SCALE>(p[i][0], nu), times<SCALE>(p[i][1], nu),
            times<SCALE>(p[i][2], nu), times<SCALE>(p[i][3], nu));
-}
-// Octet o of eight tokens of V, rows 8·o + i, chunk kb; SCALE: times the tokens' `nu` (pairs).
-// Two coordinates per turn of a rolled loop: the filling code stays in the instruction cache.
-template <int B, bool SCALE>
-__device__ __forceinline__ void put_v(const uint32_t (&w)[16], int o, uint32_t row, int kb, uint32_t lane_word,
-                                      const __half2 (&nu)[4]) {
-  uint32_t n[8], ev[4], od[4];
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    if constexpr (B == 4) n[r] = w[r];
-    else if constexpr (B == 3) n[r] = octet_nibbles(__funnelshift_r(w[r], w[8 + r], 8 * ((3 * o) & 3)) & 0xffffffu, 3);
-    else n[r] = octet_nibbles(w[r], B);
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t a = n[2 * q], b = n[2 * q + 1];
-    ev[q] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);  // coordinates 0, 2, 4, 6 of two tokens
-    od[q] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);  // 1, 3, 5, 7
-  }
-#pragma unroll 1
-  for (int i = 0; i < 8; i += 2) {
-    uint32_t p[4], r[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      p[q] = pair_of<0>(ev[q], lane_word);
-      r[q] = pair_of<0>(od[q], lane_word);
-      ev[q] >>= 8;
-      od[q] >>= 8;
-    }
-    sts_v4(row + uint32_t(i) * 128 + (uint32_t(kb ^ i) << 4), times<SCALE>(p[0], nu[0]), times<SCALE>(p[1], nu[1]),
-           times<SCALE>(p[2], nu[2]), times<SCALE>(p[3], nu[3]));
-    sts_v4(row + uint32_t(i + 1) * 128 + (uint32_t(kb ^ (i + 1)) << 4), times<SCALE>(r[0], nu[0]), times<SCALE>(r[1], nu[1]),
-           times<SCALE>(r[2], nu[2]), times<SCALE>(r[3], nu[3]));
-  }
 }
 
 // Columns [h, h + 32) of a tile: `v` where the column's token is not one of the first `valid`.
@@ -786,152 +744,88 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     }
   } else if (warp < kSoftWarps + kFillWarps) {
     // ------------------------------------------------------------ codes to fp16 levels in shared memory
-    const int ft = (tid - kSoftWarps * 32) & (kFill - 1);
+    // Four warps for K, four for V, the same code; the K side also leaves both norms for the weights.
     const bool v_side = warp >= kSoftWarps + kFillWarps / 2;
+    const int ft = (tid - kSoftWarps * 32) & (kFill - 1);
+    const int n = ft % TN, sub = ft / TN;  // row of the tile
+    const int tok = token_of(n);
+    const int bits = v_side ? a.v_bits : a.k_bits;
     const uint32_t lane_word = L::TABLE | uint32_t(lane * 4) | (v_side ? 128u : 0u);
-    // row of the cache of a tile's token t; rows past the segment's end repeat its last
-    auto row_of = [&](const Cursor& c, int t) {
-      const int tt = c.i * TN + t;
-      return int64_t(c.s.token + (tt < c.s.tokens ? tt : c.s.tokens - 1)) * a.hkv + c.s.g;
-    };
-    auto folded = [&](const Cursor& c) { return FOLD && !(D <= 128 && c.s.nrows <= kFewRows); };
+    const uint32_t piece0 = L::piece(0, v_side, tok / L::PR), maxima = v_side ? L::VOWN : L::KMAX;
     Cursor c(a, range);
+    uint32_t kw[2][4];  // rows that no box moves (d = 64)
+    float norm = 0.f, norm_v = 0.f;
+    auto fetch = [&] {  // what comes from global memory for the cursor's tile; rows past the end repeat the last
+      const int tt = c.i * TN + tok, part = c.s.flags & 1;
+      const bool in = tt < c.s.tokens;
+      const int64_t row = int64_t(c.s.token + (in ? tt : c.s.tokens - 1)) * a.hkv + c.s.g;
+      norm_v = in ? __ldg(a.v_norms[part] + row) : 0.f;
+      norm = v_side ? norm_v : __ldg(a.k_norms[part] + row);
+      if constexpr (D == 64) {
+        if (bits & 1) {
+          const uint32_t* p = reinterpret_cast<const uint32_t*>((v_side ? a.v_codes : a.k_codes)[part] + row * (D * bits / 8));
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              if (k < bits) kw[i][k] = __ldg(p + i * bits + k);
+        }
+      }
+    };
+    if (c.live()) fetch();
     bool ok = placed;
-    if (!v_side) {
-      // ---- K: one token per thread (half of one for d = 256), and the tile's norms
-      const int n = ft % TN, sub = ft / TN;  // row of the tile
-      const int tok = token_of(n);
-      uint32_t kw[2][4];  // rows that no box moves (d = 64)
-      float norm_k = 0.f, norm_v = 0.f;
-      auto fetch = [&] {  // what comes from global memory for the cursor's tile
-        const int64_t row = row_of(c, tok);
-        norm_k = __ldg(a.k_norms[c.s.flags & 1] + row);
-        norm_v = c.i * TN + tok < c.s.tokens ? __ldg(a.v_norms[c.s.flags & 1] + row) : 0.f;
-        if constexpr (D == 64) {
-          const uint8_t* kc = a.k_codes[c.s.flags & 1] + row * (D * a.k_bits / 8);
-          if (a.k_bits & 1) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int k = 0; k < 3; ++k)
-                if (k < a.k_bits) kw[i][k] = __ldg(reinterpret_cast<const uint32_t*>(kc) + i * a.k_bits + k);
-          }
-        }
-      };
-      if (c.live()) fetch();
-      for (int j = 0; c.live(); ++j) {
-        // norm slots are used every fourth tile: what read this one before was done when S
-        // of tile j − 2 began
+    for (int j = 0; c.live(); ++j) {
+      // norm slots are used every fourth tile: what read this one before was done when S of
+      // tile j − 2 began
+      const float big = warp_max(fabsf(norm));
+      if (!v_side) {
         const uint32_t slot = uint32_t(j & 3) * (TN * 4) + uint32_t(n) * 4;
-        const float vmax = warp_max(fabsf(norm_v)), kmax = warp_max(fabsf(norm_k));
+        const float vmax = warp_max(fabsf(norm_v));
         if (sub == 0) {
-          *reinterpret_cast<float*>(at(L::NK + slot)) = norm_k;
+          *reinterpret_cast<float*>(at(L::NK + slot)) = norm;
           *reinterpret_cast<float*>(at(L::NV + slot)) = norm_v;
-          if (lane == 0) {
-            *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = vmax;
-            *reinterpret_cast<float*>(at(L::KMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = kmax;
-          }
+          if (lane == 0) *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = vmax;
         }
-        ok = ok && wait_for(c_full(j), phase(j), fail) && (j < 1 || wait_for(s_full(j - 1), phase(j - 1), fail));
-        ok = meet(7, kFill, ok);
-        if (!ok) break;
-        const bool fold = folded(c);
-        const __half2 nu = __float2half2_rn(fold ? norm_k / norm_unit(tile_max<TN>(L::KMAX, j)) : 1.f);
-        auto fill = [&](auto bits) {
-          constexpr int B = decltype(bits)::value;
-          auto turns = [&](auto scale) {
-            constexpr bool SCALE = decltype(scale)::value;
-            if constexpr (kBoxed<D, B>) {
-              const uint32_t piece = L::piece(j & 1, 0, tok / L::PR);
-#pragma unroll 1
-              for (int it = sub * L::TURNS; it < (sub + 1) * L::TURNS; ++it) {
-                uint32_t w[4];
-                read_k<D, B>(piece, tok % L::PR, it, w);
-                put_k<B, SCALE>(w, L::KT + uint32_t(it >> 1) * (TN * 128) + uint32_t(n) * 128, (it & 1) * 4, n, lane_word, nu);
-              }
-            } else {
-              put_k<B, SCALE>(kw[0], L::KT + uint32_t(n) * 128, 0, n, lane_word, nu);
-              put_k<B, SCALE>(kw[1], L::KT + uint32_t(n) * 128, 4, n, lane_word, nu);
-            }
-          };
-          if (fold) turns(std::true_type{});
-          else turns(std::false_type{});
-        };
-        switch (a.k_bits) {
-          case 1: fill(std::integral_constant<int, 1>{}); break;
-          case 2: fill(std::integral_constant<int, 2>{}); break;
-          case 3: fill(std::integral_constant<int, 3>{}); break;
-          default: fill(std::integral_constant<int, 4>{}); break;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(k_full(j));
-          mbar_arrive(c_free(j));
-        }
-        c.next(a);
-        if (c.live()) fetch();
       }
-    } else {
-      // ---- V: eight tokens of one block of 64, two octets (one for d = 64)
-      constexpr int NB = TN / 64, UNITS = D == 64 ? 1 : 2;
-      const int kb = lane & 7, rest = ft >> 3;
-      const int vblock = NB == 2 ? rest >> 3 : 0, o0 = NB == 2 ? rest & 7 : rest;
-      const int v_tok = 64 * vblock + 8 * kb;
-      uint32_t vw[16];
-      auto fetch = [&] {
-        if constexpr (D == 64) {
-          if (a.v_bits & 1) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const uint8_t* vc = a.v_codes[c.s.flags & 1] + row_of(c, v_tok + ((r + kb) & 7)) * (D * a.v_bits / 8);
-              if (a.v_bits == 1) fetch_v<1>(vc, r, o0, vw);
-              else fetch_v<3>(vc, r, o0, vw);
-            }
+      if (sub == 0 && lane == 0) *reinterpret_cast<float*>(at(maxima + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = big;
+      // the codes are there; K's tile has been read by S of the last tile, V's stage by O of the last but one
+      ok = ok && wait_for(c_full(j), phase(j), fail);
+      if (v_side) ok = ok && (j < 2 || wait_for(o_done(j), phase(j - 2), fail));
+      else ok = ok && (j < 1 || wait_for(s_full(j - 1), phase(j - 1), fail));
+      ok = meet(v_side ? 8 : 7, kFill, ok);
+      if (!ok) break;
+      const bool fold = FOLD && !(D <= 128 && c.s.nrows <= kFewRows);
+      const __half2 nu = __float2half2_rn(fold ? norm / norm_unit(tile_max<TN>(maxima, j)) : 1.f);
+      const uint32_t dst = (v_side ? L::V0 + uint32_t(j & 1) * 0x8000u : L::KT) + uint32_t(n) * 128;
+      const uint32_t piece = piece0 + uint32_t(j & 1) * 0x4000u;
+      auto fill = [&](auto width) {
+        constexpr int B = decltype(width)::value;
+        if constexpr (kBoxed<D, B>) {
+#pragma unroll 1
+          for (int it = sub * L::TURNS; it < (sub + 1) * L::TURNS; ++it) {
+            uint32_t w[4];
+            read_octets<D, B>(piece, tok % L::PR, it, w);
+            put_octets<B, FOLD>(w, dst + uint32_t(it >> 1) * (TN * 128), (it & 1) * 4, n, lane_word, nu);
           }
+        } else {
+          put_octets<B, FOLD>(kw[0], dst, 0, n, lane_word, nu);
+          put_octets<B, FOLD>(kw[1], dst, 4, n, lane_word, nu);
         }
       };
-      if (c.live()) fetch();
-      for (int j = 0; c.live(); ++j) {
-        const bool fold = folded(c);
-        ok = ok && wait_for(c_full(j), phase(j), fail) && (!fold || wait_for(k_full(j), phase(j), fail)) &&
-             (j < 2 || wait_for(o_done(j), phase(j - 2), fail));
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        __half2 nu[4];
-        if (fold) {
-          const float inv = 1.f / norm_unit(tile_max<TN>(L::VMAX, j));
-          const uint32_t nv = L::NV + uint32_t((j & 3) * TN + v_tok) * 4;  // rows v_tok + r hold the tokens of w[r]
-          const float4 n0 = lds_f4(nv), n1 = lds_f4(nv + 16);
-          nu[0] = __floats2half2_rn(n0.x * inv, n0.y * inv), nu[1] = __floats2half2_rn(n0.z * inv, n0.w * inv);
-          nu[2] = __floats2half2_rn(n1.x * inv, n1.y * inv), nu[3] = __floats2half2_rn(n1.z * inv, n1.w * inv);
-        }
-        auto fill = [&](auto bits) {
-          constexpr int B = decltype(bits)::value;
-#pragma unroll 1
-          for (int u = 0; u < UNITS; ++u) {
-            const int o = o0 + u * (16 / NB);
-            if constexpr (kBoxed<D, B>) read_v<D, B>(L::piece(j & 1, 1, v_tok / L::PR), v_tok % L::PR, kb, o, vw);
-            const uint32_t row = L::V0 + uint32_t(j & 1) * 0x8000u + uint32_t(vblock) * (D * 128) + uint32_t(8 * o) * 128;
-            if (fold) put_v<B, true>(vw, o, row, kb, lane_word, nu);
-            else put_v<B, false>(vw, o, row, kb, lane_word, nu);
-          }
-        };
-        switch (a.v_bits) {
-          case 1: fill(std::integral_constant<int, 1>{}); break;
-          case 2: fill(std::integral_constant<int, 2>{}); break;
-          case 3: fill(std::integral_constant<int, 3>{}); break;
-          default: fill(std::integral_constant<int, 4>{}); break;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(v_full(j));
-          mbar_arrive(c_free(j));
-        }
-        c.next(a);
-        if (c.live()) fetch();
+      switch (bits) {
+        case 1: fill(std::integral_constant<int, 1>{}); break;
+        case 2: fill(std::integral_constant<int, 2>{}); break;
+        case 3: fill(std::integral_constant<int, 3>{}); break;
+        default: fill(std::integral_constant<int, 4>{}); break;
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(v_side ? v_full(j) : k_full(j));
+        mbar_arrive(c_free(j));
+      }
+      c.next(a);
+      if (c.live()) fetch();
     }
   } else if (warp == kSoftWarps + kFillWarps + 1) {
     // ---------------------------------------------------------------- one thread copies the packed codes
@@ -967,19 +861,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
     auto scores = [&](int jj, bool few) {
       const uint32_t d = tm + uint32_t(L::S + (jj & 1) * TN);
+      const uint64_t k0 = smem_desc_sw128(L::KT);
       if (elect_one()) {
+        if (few) {
 #pragma unroll
-      for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+          for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t k = smem_desc_sw128(L::KT + uint32_t(ks >> 2) * (TN * 128) + uint32_t(ks & 3) * 32);
-          if (few)
-            tc_mma_f16(d, k, smem_desc_sw128(L::QB + uint32_t(part * (D / 64) + (ks >> 2)) * 2048 + uint32_t(ks & 3) * 32),
-                       L::idesc(16), uint32_t(part + ks > 0));
-          else
-            tc_mma_f16_ts(d, tm + uint32_t((part ? L::QL : L::Q) + 8 * ks), k, L::idesc(TN), uint32_t(part + ks > 0));
+            for (int ks = 0; ks < D / 16; ++ks)
+              tc_mma_f16(d, k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4),
+                         smem_desc_sw128(L::QB) + uint64_t(((part * (D / 64) + (ks >> 2)) * 2048 + (ks & 3) * 32) >> 4), L::idesc(16),
+                         uint32_t(part + ks > 0));
+        } else {
+#pragma unroll
+          for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              tc_mma_f16_ts(d, tm + uint32_t((part ? L::QL : L::Q) + 8 * ks), k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4),
+                            L::idesc(TN), uint32_t(part + ks > 0));
         }
-      mma_commit(s_full(jj));
+        mma_commit(s_full(jj));
       }
       __syncwarp();
     };
@@ -1001,19 +901,21 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         ok = __all_sync(kFull, wait_for(v_full(j), phase(j), fail) && wait_for(p_full(j), phase(j), fail));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t p = tm + uint32_t(L::S + (j & 1) * TN), v = L::V0 + uint32_t(j & 1) * 0x8000u;
         if (elect_one()) {
+          const uint32_t p = tm + uint32_t(L::S + (j & 1) * TN);
+          const uint64_t v0 = smem_desc_mn128(L::V0 + uint32_t(j & 1) * 0x8000u, TN * 128);  // 16 tokens per step of 2 KB
+          if (few) {  // for d = 64 the product's rows past 64 are not read
+            const uint64_t pt = smem_desc_sw128(L::PT + uint32_t(j & 1) * 4096);
 #pragma unroll
-        for (int ks = 0; ks < TN / 16; ++ks) {
-          const uint64_t vd = smem_desc_sw128(v + uint32_t(ks >> 2) * (D * 128) + uint32_t(ks & 3) * 32);
-          if (few)  // for d = 64 the product's rows past 64 are not read
-            tc_mma_f16(tm + uint32_t(L::O), vd,
-                       smem_desc_sw128(L::PT + uint32_t(j & 1) * 4096 + uint32_t(ks >> 2) * 2048 + uint32_t(ks & 3) * 32),
-                       L::idesc(16), uint32_t(i > 0 || ks > 0));
-          else
-            tc_mma_f16_ts(tm + uint32_t(L::O), p + uint32_t(ks < TN / 32 ? 8 * ks : TN / 4 + 8 * ks), vd, L::idesc(D),
-                          uint32_t(i > 0 || ks > 0));
-        }
+            for (int ks = 0; ks < TN / 16; ++ks)
+              tc_mma_f16(tm + uint32_t(L::O), v0 + uint64_t(ks * 128), pt + uint64_t(((ks >> 2) * 2048 + (ks & 3) * 32) >> 4),
+                         L::idesc(16) | (1u << 15), uint32_t(i > 0 || ks > 0));
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < TN / 16; ++ks)
+              tc_mma_f16_ts(tm + uint32_t(L::O), p + uint32_t(ks < TN / 32 ? 8 * ks : TN / 4 + 8 * ks), v0 + uint64_t(ks * 128),
+                            L::idesc(D) | (1u << 16), uint32_t(i > 0 || ks > 0));
+          }
         mma_commit(o_done(j));
         }
         __syncwarp();
