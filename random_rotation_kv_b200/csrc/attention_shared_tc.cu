@@ -18,19 +18,19 @@
 // thread has a token's 8 rows to weigh instead of a row's 64 tokens of which most
 // rows would be empty.
 //
-// One CTA per SM walks its range of tiles (128 tokens, 64 for d = 256), 18 warps:
+// One CTA per SM walks its range of tiles (128 tokens, 64 for d = 256), 19 warps:
 //  * warp 17 copies the packed codes of two tiles ahead into shared memory (TMA boxes of
 //    half a tile's rows, swizzled where rows are 32, 64 or 128 bytes; rows of 8 and 24 bytes
 //    are not multiples of TMA's 16 and are read by the filling warps themselves);
 //  * warps 8–11 and 12–15 turn K and V codes into fp16 levels, one token per thread, by one
 //    shared-memory lookup per byte of two coordinates (tables of 256 pairs, one copy per lane
 //    so that no bank conflicts), and write rows [token][coordinate] in the 128-byte swizzle,
-//    V in two stages: as they lie, K is a K-major operand and V, whose tokens are summed over,
+//    K in two stages: as they lie, K is a K-major operand and V, whose tokens are summed over,
 //    an MN-major one.  Row 8k + e of a tile's 64 is token 8k + (e + k) mod 8, so the eight
 //    lanes that share a wavefront read eight neighbouring code rows.  For bf16 queries the
 //    norms (over their tile's unit) are multiplied in here, and for more than 16 rows they
 //    are out of the weights' way;
-//  * warp 16 issues the products; the next tile's S runs while this tile's weights are made;
+//  * warp 16 issues S, a tile ahead of the weights, and warp 18 O;
 //  * warps 0–7 make the weights: two threads per query row with half of the tokens each,
 //    the row's maximum met through shared memory, weights back into S's own columns as
 //    fp16 (or, for few rows, a thread per token and 8 rows, weights into shared memory).
@@ -50,7 +50,7 @@ constexpr uint32_t kWaitLimit = 1u << 24;  // polls, a few seconds in all
 constexpr int kSoftWarps = 8, kFillWarps = 8;
 constexpr int kFill = 128;  // threads that fill K, and as many that fill V
 constexpr int kFewRows = 16;  // rows of a unit that exchanges the operands' roles
-constexpr int kThreads = (kSoftWarps + kFillWarps + 2) * 32;
+constexpr int kThreads = (kSoftWarps + kFillWarps + 3) * 32;
 
 template <int D> struct Tc {
   static constexpr int TN = D <= 128 ? 128 : 64;     // tokens per tile
@@ -75,8 +75,8 @@ template <int D> struct Tc {
     return 0x8000u + uint32_t(stage * 4 + v * 2 + half) * 0x1000u;
   }
   static constexpr uint32_t TABLE = 0x10000;         // K pairs at +0, V pairs at +128 of every 256 bytes
-  static constexpr uint32_t KT = 0x20000;            // K tile
-  static constexpr uint32_t V0 = 0x28000;            // V stages
+  static constexpr uint32_t K0 = 0x20000;            // K stages of 32 KB
+  static constexpr uint32_t VT = 0x30000;            // V tile
   static constexpr size_t kTotal = 0x38000 - kBase;
   // tensor memory columns
   static constexpr int S = 0, O = 2 * TN, Q = O + D, QL = Q + D / 2;
@@ -775,6 +775,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (c.live()) fetch();
     bool ok = placed;
     for (int j = 0; c.live(); ++j) {
+      // the codes are there; K's stage has been read by S of the last tile but one, V's tile by
+      // O of the last
+      ok = ok && wait_for(c_full(j), phase(j), fail);
+      if (v_side) ok = ok && (j < 1 || wait_for(o_done(j - 1), phase(j - 1), fail));
+      else ok = ok && (j < 2 || wait_for(s_full(j), phase(j - 2), fail));
       // norm slots are used every fourth tile: what read this one before was done when S of
       // tile j − 2 began
       const float big = warp_max(fabsf(norm));
@@ -788,15 +793,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         }
       }
       if (sub == 0 && lane == 0) *reinterpret_cast<float*>(at(maxima + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = big;
-      // the codes are there; K's tile has been read by S of the last tile, V's stage by O of the last but one
-      ok = ok && wait_for(c_full(j), phase(j), fail);
-      if (v_side) ok = ok && (j < 2 || wait_for(o_done(j), phase(j - 2), fail));
-      else ok = ok && (j < 1 || wait_for(s_full(j - 1), phase(j - 1), fail));
       ok = meet(v_side ? 8 : 7, kFill, ok);
       if (!ok) break;
       const bool fold = FOLD && !(D <= 128 && c.s.nrows <= kFewRows);
       const __half2 nu = __float2half2_rn(fold ? norm / norm_unit(tile_max<TN>(maxima, j)) : 1.f);
-      const uint32_t dst = (v_side ? L::V0 + uint32_t(j & 1) * 0x8000u : L::KT) + uint32_t(n) * 128;
+      const uint32_t dst = (v_side ? L::VT : L::K0 + uint32_t(j & 1) * 0x8000u) + uint32_t(n) * 128;
       const uint32_t piece = piece0 + uint32_t(j & 1) * 0x4000u;
       auto fill = [&](auto width) {
         constexpr int B = decltype(width)::value;
@@ -853,78 +854,74 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(c_full(k), phase(k)); ++i) {
         }
     }
-  } else if (warp == kSoftWarps + kFillWarps) {
-    // ---------------------------------------------------------------- products; the warp stays together, one thread issues
+  } else {
+    // ---------------------------------------------------------------- products; the warps stay together, one thread issues
+    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+    const bool o_side = warp == kSoftWarps + kFillWarps + 2;
     Cursor c(a, range);
     int j = 0, seg = 0;
     bool ok = placed;
-    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-    auto scores = [&](int jj, bool few) {
-      const uint32_t d = tm + uint32_t(L::S + (jj & 1) * TN);
-      const uint64_t k0 = smem_desc_sw128(L::KT);
-      if (elect_one()) {
-        if (few) {
-#pragma unroll
-          for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              tc_mma_f16(d, k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4),
-                         smem_desc_sw128(L::QB) + uint64_t(((part * (D / 64) + (ks >> 2)) * 2048 + (ks & 3) * 32) >> 4), L::idesc(16),
-                         uint32_t(part + ks > 0));
-        } else {
-#pragma unroll
-          for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              tc_mma_f16_ts(d, tm + uint32_t((part ? L::QL : L::Q) + 8 * ks), k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4),
-                            L::idesc(TN), uint32_t(part + ks > 0));
-        }
-        mma_commit(s_full(jj));
-      }
-      __syncwarp();
-    };
-    while (ok && c.live()) {
+    for (; ok && c.live(); c.next_segment(a), ++seg) {
       const int tiles = c.s.tiles;
       const bool few = D <= 128 && c.s.nrows <= kFewRows;
-      ok = __all_sync(kFull, wait_for(q_full, uint32_t(seg) & 1u, fail) && wait_for(k_full(j), phase(j), fail));
-      if (!ok) break;
-      tc_fence_after();
-      scores(j, few);
-      for (int i = 0; i < tiles; ++i, ++j) {
-        if (i + 1 < tiles) {
-          ok = __all_sync(kFull, wait_for(k_full(j + 1), phase(j + 1), fail) &&
-                                     (j < 1 || wait_for(o_done(j - 1), phase(j - 1), fail)));
+      if (!o_side) {
+        ok = __all_sync(kFull, wait_for(q_full, uint32_t(seg) & 1u, fail));
+        for (int i = 0; ok && i < tiles; ++i, ++j) {
+          // K is there, and the weights of the last tile but one have left the columns of its S
+          ok = __all_sync(kFull, wait_for(k_full(j), phase(j), fail) && (j < 2 || wait_for(o_done(j), phase(j - 2), fail)));
           if (!ok) break;
           tc_fence_after();
-          scores(j + 1, few);
-        }
-        ok = __all_sync(kFull, wait_for(v_full(j), phase(j), fail) && wait_for(p_full(j), phase(j), fail));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t p = tm + uint32_t(L::S + (j & 1) * TN);
-          const uint64_t v0 = smem_desc_mn128(L::V0 + uint32_t(j & 1) * 0x8000u, TN * 128);  // 16 tokens per step of 2 KB
-          if (few) {  // for d = 64 the product's rows past 64 are not read
-            const uint64_t pt = smem_desc_sw128(L::PT + uint32_t(j & 1) * 4096);
+          if (elect_one()) {
+            const uint32_t d = tm + uint32_t(L::S + (j & 1) * TN);
+            const uint64_t k0 = smem_desc_sw128(L::K0 + uint32_t(j & 1) * 0x8000u);
+            if (few) {
 #pragma unroll
-            for (int ks = 0; ks < TN / 16; ++ks)
-              tc_mma_f16(tm + uint32_t(L::O), v0 + uint64_t(ks * 128), pt + uint64_t(((ks >> 2) * 2048 + (ks & 3) * 32) >> 4),
-                         L::idesc(16) | (1u << 15), uint32_t(i > 0 || ks > 0));
-          } else {
+              for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
-            for (int ks = 0; ks < TN / 16; ++ks)
-              tc_mma_f16_ts(tm + uint32_t(L::O), p + uint32_t(ks < TN / 32 ? 8 * ks : TN / 4 + 8 * ks), v0 + uint64_t(ks * 128),
-                            L::idesc(D) | (1u << 16), uint32_t(i > 0 || ks > 0));
+                for (int ks = 0; ks < D / 16; ++ks)
+                  tc_mma_f16(d, k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4),
+                             smem_desc_sw128(L::QB) + uint64_t(((part * (D / 64) + (ks >> 2)) * 2048 + (ks & 3) * 32) >> 4),
+                             L::idesc(16), uint32_t(part + ks > 0));
+            } else {
+#pragma unroll
+              for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                  tc_mma_f16_ts(d, tm + uint32_t((part ? L::QL : L::Q) + 8 * ks),
+                                k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), L::idesc(TN), uint32_t(part + ks > 0));
+            }
+            mma_commit(s_full(j));
           }
-        mma_commit(o_done(j));
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+        for (int i = 0; ok && i < tiles; ++i, ++j) {
+          ok = __all_sync(kFull, wait_for(v_full(j), phase(j), fail) && wait_for(p_full(j), phase(j), fail));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t p = tm + uint32_t(L::S + (j & 1) * TN);
+            const uint64_t v0 = smem_desc_mn128(L::VT, TN * 128);  // 16 tokens per step of 2 KB
+            if (few) {  // for d = 64 the product's rows past 64 are not read
+              const uint64_t pt = smem_desc_sw128(L::PT + uint32_t(j & 1) * 4096);
+#pragma unroll
+              for (int ks = 0; ks < TN / 16; ++ks)
+                tc_mma_f16(tm + uint32_t(L::O), v0 + uint64_t(ks * 128), pt + uint64_t(((ks >> 2) * 2048 + (ks & 3) * 32) >> 4),
+                           L::idesc(16) | (1u << 15), uint32_t(i > 0 || ks > 0));
+            } else {
+#pragma unroll
+              for (int ks = 0; ks < TN / 16; ++ks)
+                tc_mma_f16_ts(tm + uint32_t(L::O), p + uint32_t(ks < TN / 32 ? 8 * ks : TN / 4 + 8 * ks), v0 + uint64_t(ks * 128),
+                              L::idesc(D) | (1u << 16), uint32_t(i > 0 || ks > 0));
+            }
+            mma_commit(o_done(j));
+          }
+          __syncwarp();
+        }
       }
-      ++seg;
-      c.next_segment(a);
     }
     // products still in flight end before the tensor memory is given up
-    uint64_t* drain = &bars[11];
+    uint64_t* drain = &bars[o_side ? 16 : 11];
     if (elect_one()) {
       mbar_init(drain, 1);
       fence_mbarrier_init();
