@@ -44,33 +44,28 @@ template <int N> __device__ __forceinline__ void fwht_row(float (&v)[N], int lan
 
 // ---- the line of tiles, by one block of 256 threads.  A unit's parts are the ranges that
 // its tiles' costs fall into; part in range r of the U-th non-empty unit is segment U + r,
-// as each range before r adds at most one segment to those of the units before.
-__device__ void lay_out_unit(const SharedArgs& a, SharedSegment s, int tiles, int tokens, int unit, int units, int64_t cost,
-                             int64_t next, int tile_cost, int per, int first_part, int* count) {
-  const int r0 = int(cost / per), r1 = int((cost + int64_t(tiles - 1) * tile_cost) / per);
-  const int rn = unit + 1 < units ? int(next / per) : -1;  // the next unit's first range
-  const int token = s.token, tail = s.flags, g = s.g;
-  int at = 0;
-  for (int r = r0; r <= r1; ++r) {
-    const int end = r == r1 ? tiles : int((int64_t(r + 1) * per - cost + tile_cost - 1) / tile_cost);
-    s.token = token + at * a.tile;
-    s.tokens = (end * a.tile < tokens ? end * a.tile : tokens) - at * a.tile;
-    s.tiles = end - at;
-    s.state = (first_part + r - r0) * a.hkv + g;
-    s.flags = tail | (r < r1 || rn != r ? 2 : 0);
-    a.segs[2 * (unit + r)] = make_int4(s.token, s.tokens, s.tiles, s.g);
-    a.segs[2 * (unit + r) + 1] = make_int4(s.row0, s.nrows, s.state, s.flags);
-    if (r > r0 || unit == 0) a.begin[r] = unit + r;
-    at = end;
-  }
-  if (rn > r1) a.begin[rn] = unit + 1 + rn;
-  *count = r1 - r0 + 1;
+// as each range before r adds at most one segment to those of the units before.  All costs
+// are below 2^30.
+__device__ __forceinline__ void put_segment(const SharedArgs& a, int index, const SharedSegment& s) {
+  a.segs[2 * index] = make_int4(s.token, s.tokens, s.tiles, s.g);
+  a.segs[2 * index + 1] = make_int4(s.row0, s.nrows, s.state, s.flags);
+}
+// Tiles [at, end) of a unit of `tokens` tokens (its token 0 in s.token) as part `part`.
+__device__ __forceinline__ void put_part(const SharedArgs& a, int index, SharedSegment s, int at, int end, int tokens, int part,
+                                         bool last) {
+  s.token += at * a.tile;
+  s.tokens = (end * a.tile < tokens ? end * a.tile : tokens) - at * a.tile;
+  s.tiles = end - at;
+  s.state = part * a.hkv + s.g;
+  s.flags |= last ? 2 : 0;
+  put_segment(a, index, s);
 }
 
 __device__ void lay_out(const SharedArgs& a) {
   __shared__ int2 s_sum[8];
+  __shared__ int4 s_tail[256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int r = tid; r < a.grid; r += 256) a.begin[r] = -1;
+  for (int r = tid; r < a.grid; r += 256) a.begin[r] = -1;  // the barrier below comes before the others' entries
   // tokens and tiles of a sequence's tail
   auto length = [&](int64_t b) {
     if (b >= a.batch || a.lens == nullptr) return 0;
@@ -91,19 +86,32 @@ __device__ void lay_out(const SharedArgs& a) {
   tiles = filled = 0;
 #pragma unroll
   for (int w = 0; w < 8; ++w) tiles += s_sum[w].x, filled += s_sum[w].y;
-  const int64_t pcost = int64_t(a.units_p) * a.ptiles * a.pcost;
-  const int64_t cost = pcost + int64_t(a.hkv) * (int64_t(tiles) * a.tcost + int64_t(filled) * a.scost);
-  const int64_t even = (cost + a.grid - 1) / a.grid;
-  const int per = int(even < a.min_cost ? a.min_cost : even);
+  const int pcost = a.units_p * a.ptiles * a.pcost;
+  const int cost = pcost + a.hkv * (tiles * a.tcost + filled * a.scost);
+  const int even = (cost + a.grid - 1) / a.grid;
+  const int per = even < a.min_cost ? a.min_cost : even;
   const int units = a.units_p + a.hkv * filled;
-  for (int u = tid; u < a.units_p; u += 256) {
-    SharedSegment s = {};
-    s.g = u / a.row_tiles;
-    s.row0 = (u % a.row_tiles) * 128;
-    s.nrows = int(a.rows - s.row0 < 128 ? a.rows - s.row0 : 128);
-    const int64_t at = int64_t(u) * a.ptiles * a.pcost;
-    lay_out_unit(a, s, a.ptiles, int(a.prefix), u, units, at, at + int64_t(a.ptiles) * a.pcost, a.pcost, per, 0, a.counts + u);
+  // the prefix, a thread per range: its tiles of one prefix unit after the other
+  const int ptotal = a.units_p * a.ptiles;
+  for (int r = tid; r < a.grid && ptotal > 0; r += 256) {
+    int pos = (r * per + a.pcost - 1) / a.pcost, end = ((r + 1) * per + a.pcost - 1) / a.pcost;
+    if (end > ptotal) end = ptotal;
+    const bool more = units > a.units_p && pcost / per == r;  // the first tail begins in this range
+    if (pos < end) a.begin[r] = pos / a.ptiles + r;
+    while (pos < end) {
+      const int u = pos / a.ptiles, at = pos - u * a.ptiles;
+      const int to = end - u * a.ptiles < a.ptiles ? end - u * a.ptiles : a.ptiles;
+      SharedSegment s = {};
+      s.g = u / a.row_tiles;
+      s.row0 = (u - s.g * a.row_tiles) * 128;
+      s.nrows = int(a.rows - s.row0 < 128 ? a.rows - s.row0 : 128);
+      const int r0 = u * a.ptiles * a.pcost / per;
+      pos += to - at;
+      put_part(a, u + r, s, at, to, int(a.prefix), r - r0, pos == end && !more);
+      if (to == a.ptiles) a.counts[u] = r - r0 + 1;
+    }
   }
+  // the tails, a thread per sequence and kv head
   int before = 0, some_before = 0;
   for (int64_t b0 = 0; b0 < a.batch && a.cap > 0; b0 += 256) {
     const int64_t b = b0 + tid;
@@ -125,27 +133,42 @@ __device__ void lay_out(const SharedArgs& a) {
       all += x.x;
       all_some += x.y;
     }
-    const int tiles_before = before + sum - mine, units_before = some_before + some - (mine > 0);
+    s_tail[tid] = make_int4(before + sum - mine, some_before + some - (mine > 0), len, mine);
     before += all;
     some_before += all_some;
-    if (b >= a.batch) continue;
-    for (int g = 0; g < a.hkv; ++g) {
-      int* count = a.counts + a.units_p + b * a.hkv + g;
-      if (mine == 0) {
+    __syncthreads();
+    const int here = int(a.batch - b0 < 256 ? a.batch - b0 : 256) * a.hkv;
+    for (int k = tid; k < here; k += 256) {
+      const int bb = k / a.hkv, g = k - bb * a.hkv;
+      const int4 t = s_tail[bb];  // tiles and non-empty tails before it, tokens, tiles
+      int* count = a.counts + a.units_p + b0 * a.hkv + k;
+      if (t.w == 0) {
         *count = 0;
         continue;
       }
       SharedSegment s = {};
-      s.token = int(b * a.cap);
+      s.token = int((b0 + bb) * a.cap);
       s.g = g;
-      s.row0 = int(b * a.group);
+      s.row0 = int((b0 + bb) * a.group);
       s.nrows = a.group;
       s.flags = 1;
-      const int64_t at = pcost + (int64_t(a.hkv) * tiles_before + int64_t(g) * mine) * a.tcost +
-                         (int64_t(a.hkv) * units_before + g) * a.scost;
-      lay_out_unit(a, s, mine, len, a.units_p + a.hkv * units_before + g, units, at, at + int64_t(mine) * a.tcost + a.scost, a.tcost,
-                   per, a.parts_p, count);
+      const int unit = a.units_p + a.hkv * t.y + g;
+      const int from = pcost + (a.hkv * t.x + g * t.w) * a.tcost + (a.hkv * t.y + g) * a.scost;
+      const int r0 = from / per, r1 = (from + (t.w - 1) * a.tcost) / per;
+      const int rn = unit + 1 < units ? (from + t.w * a.tcost + a.scost) / per : -1;  // the next unit's first range
+      int done = 0;
+      for (int r = r0; r <= r1; ++r) {
+        const int end = r == r1 ? t.w : ((r + 1) * per - from + a.tcost - 1) / a.tcost;
+        put_part(a, unit + r, s, done, end, t.z, a.parts_p + r - r0, r < r1 || rn != r);
+        if (r > r0 || unit == 0) a.begin[r] = unit + r;
+        done = end;
+      }
+      // a range that begins with this unit or with the next one
+      if (unit == a.units_p && unit > 0 && (pcost - a.pcost) / per < r0) a.begin[r0] = unit + r0;
+      if (rn > r1) a.begin[rn] = unit + 1 + rn;
+      *count = r1 - r0 + 1;
     }
+    __syncthreads();
   }
 }
 
@@ -275,17 +298,20 @@ __global__ void __launch_bounds__(256) shared_partial_kernel(const SharedArgs a)
   }
 }
 
-// ---- one warp per query row: its parts merged, rotated back, rounded to the output type
-template <int D>
+// ---- W warps per query row: its parts merged, rotated back, rounded to the output type.  Each
+// warp takes every W-th part; with W = 8 (calls of few rows, where latency counts) the
+// warps' sums meet in shared memory.
+template <int D, int W>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
   constexpr int N = D / 32;
+  __shared__ float s_sum[W > 1 ? W : 1][W > 1 ? D : 1], s_l[8];
   pdl_release();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);  // b·hq + h
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = W > 1 ? warp : 0;
+  const int64_t row = W > 1 ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + warp;  // b·hq + h
   if (row >= a.batch * a.hq) return;
   const int64_t b = row / a.hq;
-  const int h = int(row % a.hq), g = h / a.group;
+  const int h = int(row - b * a.hq), g = h / a.group;
   const int64_t r = b * a.group + h % a.group;
   // parts of the prefix, of the tail
   const int np = a.units_p > 0 ? a.counts[g * a.row_tiles + int(r / 128)] : 0;
@@ -294,26 +320,67 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
     const int p = i < np ? i : a.parts_p + (i - np);
     return (int64_t(p) * a.hkv + g) * a.rows + r;
   };
+  const int n = np + nt;
   float m = -INFINITY;
-  for (int i = lane; i < np + nt; i += 32) m = fmaxf(m, a.stats[state(i)].x);
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.stats[state(i)].x);
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  // lane i takes part mine + W·i; the parts' sums come in batches of independent loads
+  constexpr int kBatch = W > 1 ? 4 : N <= 4 ? 8 : 4;
   float v[N], l = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int i = 0; i < np + nt; ++i) {
-    const int64_t st = state(i);
-    const float2 ml = a.stats[st];
-    const float f = exp2f(ml.x - m);
-    l = fmaf(ml.y, f, l);
+  for (int i0 = mine; i0 < n; i0 += 32 * W) {
+    float f = 0.f;
+    int64_t st = state(i0);
+    const int i = i0 + lane * W;
+    if (i < n) {
+      st = state(i);
+      const float2 ml = a.stats[st];
+      f = exp2f(ml.x - m);
+      l = fmaf(ml.y, f, l);
+    }
+    const int left = (n - i0 + W - 1) / W, here = left < 32 ? left : 32;
+    for (int k0 = 0; k0 < here; k0 += kBatch) {
+      float x[kBatch][N], fk[kBatch];
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = fmaf(a.acc[st * D + 32 * k + lane], f, v[k]);
+      for (int k = 0; k < kBatch; ++k) {
+        const int from = k0 + k < here ? k0 + k : 0;
+        const int64_t at = __shfl_sync(kFull, st, from) * D + lane;
+        fk[k] = __shfl_sync(kFull, f, from);
+        if (k0 + k >= here) fk[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[k][e] = k0 + k < here ? a.acc[at + 32 * e] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = fmaf(x[k][e], fk[k], v[e]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s_sum[warp][32 * e + lane] = v[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    l = s_l[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) l += s_l[w];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+#pragma unroll
+      for (int w = 1; w < W; ++w) v[e] += s_sum[w][32 * e + lane];
+    }
   }
   fwht_row(v, lane);
-  const float inv = np + nt > 0 ? 1.f / (l * float(D) * a.v_alpha) : 0.f;
+  const float inv = n > 0 ? 1.f / (l * float(D) * a.v_alpha) : 0.f;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int c = 32 * k + lane;
-    const float y = np + nt > 0 ? (sign_bit(a.v_seed, c) ? -v[k] : v[k]) * inv : 0.f;
+    const float y = n > 0 ? (sign_bit(a.v_seed, c) ? -v[k] : v[k]) * inv : 0.f;
     if (a.bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + c] = __float2bfloat16_rn(y);
     else static_cast<__half*>(a.out)[row * D + c] = __float2half_rn(y);
   }
@@ -339,7 +406,9 @@ template <int D> cudaError_t launch_d(const SharedArgs& a, cudaStream_t stream) 
     e = launch_shared_tc(a, stream);
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(shared_merge_kernel<D>, blocks, dim3(256), 0, stream, a);
+  // eight warps per row while that leaves fewer than eight blocks per SM
+  if (rows <= 148 * 8) return launch_pdl(shared_merge_kernel<D, 8>, dim3(unsigned(rows)), dim3(256), 0, stream, a);
+  return launch_pdl(shared_merge_kernel<D, 1>, blocks, dim3(256), 0, stream, a);
 }
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
