@@ -594,9 +594,12 @@ namespace {
 // the whole turns before it.
 uint64_t turns_of(double f) {
   static const uint64_t kInvTwoPi[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
-  int ex = 0;
-  const double m = std::frexp(std::fabs(f), &ex);  // |f| = m·2^ex, 0.5 ≤ m < 1
-  const uint64_t sig = static_cast<uint64_t>(std::ldexp(m, 53));  // |f| = sig·2^(ex − 53)
+  uint64_t word;
+  std::memcpy(&word, &f, 8);
+  const int be = static_cast<int>(word >> 52 & 0x7ff);
+  if (be == 0) return 0;  // zero and subnormal: less than half a unit
+  const uint64_t sig = (word & 0xfffffffffffffull) | 0x10000000000000ull;  // |f| = sig·2^(ex − 53)
+  const int ex = be - 1022;
   uint64_t limb[6] = {0, 0, 0, 0, 0, 0};
   unsigned __int128 carry = 0;
   for (int k = 0; k < 3; ++k) {

@@ -17,18 +17,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two halves, with work between them that the other CTAs need not wait for.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The 32-bit word at this CTA's shared address `addr` in the CTA of rank `rank`.
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
   uint32_t v, a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
-}
-
-// Words `addr` of the first `size` (at most 16) CTAs, their loads in flight together; 0 for the others.
-__device__ __forceinline__ void ld_cluster_all(uint32_t addr, int size, uint32_t (&v)[16]) {
-#pragma unroll
-  for (int c = 0; c < 16; ++c) v[c] = c < size ? ld_cluster(addr, uint32_t(c)) : 0u;
 }
 
 // Lets `kernel` run with `smem` bytes and in clusters of 16, once per device (`done`: a bit per

@@ -6,8 +6,8 @@
 // (runs of several tiles are read again for every pass).  A key is the mass as an unsigned
 // integer of the same order; the sink and the recent tokens have the largest key.  The
 // keep-th largest key is found by radix selection: four passes over 8-bit digits from the
-// top, each a histogram per CTA (eight copies by lane, as few digits are in use and equal
-// ones would queue), the CTAs' histograms summed through distributed shared memory by every
+// top, each a histogram per CTA (in eight copies by lane: few digits are in use and equal ones
+// would queue), the CTAs' histograms summed through distributed shared memory by every
 // CTA for itself.  Then every warp counts the keys above and equal to it in its run, the
 // counts' prefixes give each kept token its slot, and of the equal ones the first are
 // kept; so the order of blocks and atomics never shows in the result.  The passes are bound
@@ -24,7 +24,6 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kPer = 16;                      // tokens per lane and tile
 constexpr int kTile = kThreads * kPer;        // tokens per tile
-constexpr int kCopies = 8;                    // of a histogram
 
 __device__ __forceinline__ int64_t clamp_len(const int32_t* lens, int64_t b, int64_t cap) {
   if (lens == nullptr) return cap;
@@ -39,10 +38,11 @@ __device__ __forceinline__ uint32_t mass_key(float v) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// REG: a CTA's run is one tile, read once.
+// REG: a CTA's run is one tile, read once.  Two CTAs per SM: of clusters of 16 with one, only 7
+// run at a time (the SMs of a GPC).
 template <bool REG>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a, int chunk, int size) {
-  __shared__ uint32_t s_copy[kCopies][256];
+__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictArgs a, int chunk, int size) {
+  __shared__ __align__(16) uint32_t s_copy[256][8];  // [digit][lane mod 8]
   __shared__ uint32_t s_hist[2][256];   // alternating passes: the other one may still be read
   __shared__ uint32_t s_sum[256];
   __shared__ uint32_t s_pick[2];        // digit, how many of its keys are kept
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
-    for (int i = tid; i < kCopies * 256; i += kThreads) s_copy[i >> 8][i & 255] = 0;
+    reinterpret_cast<uint4*>(s_copy)[tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     for (int tile = 0; tile < tiles; ++tile) {
       if constexpr (!REG) load(tile * kTile);
@@ -99,23 +99,30 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       for (int i = 0; i < kPer; ++i) {
         const uint32_t k = key_of(tile * kTile, i);
         if (tile * kTile + first + 32 * i < mine && (k & mask) == prefix)
-          atomicAdd(&s_copy[lane & (kCopies - 1)][(k >> shift) & 255u], 1u);
+          atomicAdd(&s_copy[(k >> shift) & 255u][lane & 7], 1u);
       }
     }
     __syncthreads();
-    if (tid < 256) {
-      uint32_t sum = 0;
-#pragma unroll
-      for (int c = 0; c < kCopies; ++c) sum += s_copy[c][tid];
-      s_hist[pass & 1][tid] = sum;
+    {
+      // two threads per digit
+      const uint4 c = reinterpret_cast<const uint4*>(s_copy)[tid];
+      uint32_t sum = c.x + c.y + c.z + c.w;
+      sum += __shfl_xor_sync(kFull, sum, 1);
+      if (!(tid & 1)) s_hist[pass & 1][tid >> 1] = sum;
     }
     cluster_sync();
-    if (tid < 256) {
-      uint32_t h[16], sum = 0;
-      ld_cluster_all(smem_addr(&s_hist[pass & 1][tid]), size, h);
+    {
+      // two threads per digit, the even and the odd CTAs
+      uint32_t h[8], sum = 0;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) sum += h[c];
-      s_sum[tid] = sum;
+      for (int c = 0; c < 8; ++c) {
+        const int from = 2 * c + (tid & 1);
+        h[c] = from < size ? ld_cluster(smem_addr(&s_hist[pass & 1][tid >> 1]), uint32_t(from)) : 0u;
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum += h[c];
+      sum += __shfl_xor_sync(kFull, sum, 1);
+      if (!(tid & 1)) s_sum[tid >> 1] = sum;
     }
     __syncthreads();
     if (warp == 0) {
@@ -176,6 +183,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     cluster_sync();
     before_a = __reduce_add_sync(kFull, lane < rank ? ld_cluster(smem_addr(&s_count[0]), uint32_t(lane)) : 0u);
     before_e = __reduce_add_sync(kFull, lane < rank ? ld_cluster(smem_addr(&s_count[1]), uint32_t(lane)) : 0u);
+    cluster_arrive();  // this warp has read its counts
   }
   const unsigned below = (1u << lane) - 1u;
   for (int tile = 0; tile < tiles; ++tile) {
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       pe += __popc(be);
     }
   }
-  cluster_sync();  // no CTA leaves while its counts are read
+  cluster_wait();  // no CTA leaves while its counts are read
 }
 
 // Rows [kept token][kv head] of every sequence, 128 per block and step.  U: bytes per copy.

@@ -103,21 +103,14 @@ __global__ void __launch_bounds__(kThreads) rope8_kernel(const RopeArgs a, const
   const int64_t base = (t * a.heads + h0) * a.d;
   const T* x = static_cast<const T*>(a.x) + base;
   T* y = static_cast<T*>(a.y) + base;
-  if (!turn) {
-    if (a.x == a.y) return;
-    for (int h = h0; h < h1; ++h, x += a.d, y += a.d) {
-      uint32_t p[W], q[W];
-      ld_words(x + c0, p);
-      ld_words(x + c1, q);
-      st_words(y + c0, p);
-      st_words(y + c1, q);
-    }
-    return;
-  }
+  if (!turn && a.x == a.y) return;
   float2 cs[8];
-  const int64_t pos = a.positions[t];
+  if (turn) {
+    const int64_t pos = a.positions[t];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) cs[k] = turn_of(s_turns[8 * u + k], pos, a.cos_factor, a.sin_factor);
+    for (int k = 0; k < 8; ++k) cs[k] = turn_of(s_turns[8 * u + k], pos, a.cos_factor, a.sin_factor);
+  }
+  // the same loads and stores for turned and copied runs, whose threads share warps
   constexpr int kAhead = W == 8 ? 2 : 4;  // heads whose loads are in flight together
   for (int h = h0; h < h1; h += kAhead, x += kAhead * a.d, y += kAhead * a.d) {
     uint32_t p[kAhead][W], q[kAhead][W];
@@ -130,19 +123,21 @@ __global__ void __launch_bounds__(kThreads) rope8_kernel(const RopeArgs a, const
 #pragma unroll
     for (int e = 0; e < kAhead; ++e)
       if (h + e < h1) {
-        float v0[8], v1[8];
-        to_float<T, W>(p[e], v0);
-        to_float<T, W>(q[e], v1);
+        if (turn) {
+          float v0[8], v1[8];
+          to_float<T, W>(p[e], v0);
+          to_float<T, W>(q[e], v1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float& va = INTER ? (k < 4 ? v0[2 * k] : v1[2 * k - 8]) : v0[k];
-          float& vb = INTER ? (k < 4 ? v0[2 * k + 1] : v1[2 * k - 7]) : v1[k];
-          const float r = va * cs[k].x - vb * cs[k].y;
-          vb = va * cs[k].y + vb * cs[k].x;
-          va = r;
+          for (int k = 0; k < 8; ++k) {
+            float& va = INTER ? (k < 4 ? v0[2 * k] : v1[2 * k - 8]) : v0[k];
+            float& vb = INTER ? (k < 4 ? v0[2 * k + 1] : v1[2 * k - 7]) : v1[k];
+            const float r = va * cs[k].x - vb * cs[k].y;
+            vb = va * cs[k].y + vb * cs[k].x;
+            va = r;
+          }
+          from_float<T, W>(v0, p[e]);
+          from_float<T, W>(v1, q[e]);
         }
-        from_float<T, W>(v0, p[e]);
-        from_float<T, W>(v1, q[e]);
         st_words(y + e * a.d + c0, p[e]);
         st_words(y + e * a.d + c1, q[e]);
       }
