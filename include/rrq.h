@@ -347,8 +347,9 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  * Per head the output is within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is
  * rounded to q_dtype.
  * Errors: RRQ_ERR_INVALID (incl. a workspace that is too small), RRQ_ERR_UNSUPPORTED
- * (q_dtype RRQ_F32, more than 128 heads per kv head, 2^31 or more tokens in a cache,
- * about 10^8 or more 64-token tiles over all kv heads, or a device whose per-block reserved shared memory is not the 1 KB that the tensor-core
+ * (q_dtype RRQ_F32, more than 128 heads per kv head, 2^31 − 128 or more tokens in the
+ * prefix or over all tails, 10^8 or more tiles of 64 or 128 tokens over all units of work,
+ * or a device whose per-block reserved shared memory is not the 1 KB that the tensor-core
  * kernel's layout assumes), RRQ_ERR_CUDA.
  */
 int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,

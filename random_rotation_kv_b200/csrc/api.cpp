@@ -483,7 +483,6 @@ int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,
   a.v_seed = v_seed;
   a.kscale = static_cast<float>(double(scale) * 1.4426950408889634074 / d);
   // fp16 queries: a second fp16 part keeps what the rotation would lose; bf16 ones have less to lose
-  a.split = q_dtype == RRQ_F16 && d <= 128;
   rrq::attention_shared_levels(&a, k_codebook == nullptr, v_codebook == nullptr);
   const cudaError_t e = rrq::launch_attention_shared(a, as_stream(stream));
   return e == cudaErrorNotSupported ? RRQ_ERR_UNSUPPORTED : status_of(e);

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(256) shared_prepare_kernel(const SharedArgs a)
       const float x = v[i] * f;
       const __half hi = __float2half_rn(x);
       a.qh[to * D + 32 * i + lane] = hi;
-      if (a.split) a.ql[to * D + 32 * i + lane] = __float2half_rn(x - __half2float(hi));
+      if constexpr (D <= 128) a.ql[to * D + 32 * i + lane] = __float2half_rn(x - __half2float(hi));
     }
   }
 }
@@ -420,8 +420,9 @@ bool attention_shared_plan(SharedArgs* a) {
   if (a->group > 128) return false;
   a->tile = a->d <= 128 ? 128 : 64;
   const int64_t most = int64_t(1) << 30;  // tiles of all units, in cost
-  // the tensor maps count a cache's tokens in 32 bits
-  if (a->prefix >= 2 * most || (a->batch > 0 && a->cap >= 2 * most / a->batch)) return false;
+  // a cache's tokens, rounded up to a tile, are counted in 32 bits
+  const int64_t tokens = 2 * most - 128;
+  if (a->prefix >= tokens || (a->batch > 0 && a->cap >= tokens / a->batch)) return false;
   if (a->prefix / 64 >= most || a->cap / 64 >= most || a->batch >= most / a->hq) return false;
   a->rows = a->batch * a->group;
   a->row_tiles = int((a->rows + 127) / 128);

@@ -47,14 +47,13 @@ struct SharedArgs {
   // largest level into [1, 2), times, for the default codebooks, the factor in [1, 2)
   // for which the rounded levels are nearest to the exact ones.
   float k_alpha, v_alpha;
-  int split;             // queries as two fp16 parts
   // workspace
   int* begin;     // [grid] a range's first segment, −1 for a range without tiles
   int* counts;    // [units] parts of every unit: prefix units (g · row_tiles + rt), then tails (b · hkv + g)
   int4* segs;     // two words per segment, those of a range one after the other (SharedSegment)
   float* qrot;    // rotated queries, row (g·rows + r), d values (d = 512), or in their place
   __half* qh;     //   the same as fp16 times a power of two per row,
-  __half* ql;     //   what that rounding left, when split,
+  __half* ql;     //   what that rounding left (d ≤ 128),
   float* qexp;    //   and the power of two taken out
   float2* stats;  // (m, l) of part p, kv head g, row r at (p·hkv + g)·rows + r; prefix parts, then tail parts
   float* acc;     // the same rows × d

@@ -2,9 +2,9 @@
 // 5th-generation tensor cores, for head sizes up to 256: up to 128 query rows against a
 // run of tiles of one kv head (attention_shared.h).
 //
-// With the rows' rotated queries q' (fp16, a power of two 2^-e per row taken out; for
-// fp16 queries at d ≤ 128 a second fp16 part holds what the first rounds off) and the
-// levels c as fp16,
+// With the rows' rotated queries q' (fp16, a power of two 2^-e per row taken out; at
+// d ≤ 128 a second fp16 part holds what the first rounds off, which at d = 256 the tensor
+// memory has no room for) and the levels c as fp16,
 //     S = Q'·C_Kᵀ,   x = 2^e·ν^K_t·S,   P = 2^{x − m'}·ν^V_t,   O += P·C_V,
 // where m' follows the row's running maximum m: it moves only when m grows by more than
 // 4 (powers of two), so O is rarely rescaled, and it carries the power of two that
@@ -27,9 +27,7 @@
 //    so that no bank conflicts), and write rows [token][coordinate] in the 128-byte swizzle,
 //    K in two stages: as they lie, K is a K-major operand and V, whose tokens are summed over,
 //    an MN-major one.  Row 8k + e of a tile's 64 is token 8k + (e + k) mod 8, so the eight
-//    lanes that share a wavefront read eight neighbouring code rows.  For bf16 queries the
-//    norms (over their tile's unit) are multiplied in here, and for more than 16 rows they
-//    are out of the weights' way;
+//    lanes that share a wavefront read eight neighbouring code rows;
 //  * warp 16 issues S, a tile ahead of the weights, and warp 18 O;
 //  * warps 0–7 make the weights: two threads per query row with half of the tokens each,
 //    the row's maximum met through shared memory, weights back into S's own columns as
@@ -63,8 +61,6 @@ template <int D> struct Tc {
   static constexpr uint32_t TSLOT = 0x4C0;
   static constexpr uint32_t FAIL = 0x4D0;
   static constexpr uint32_t VMAX = 0x500;            // [4 tiles][4 warps] largest value norm
-  static constexpr uint32_t KMAX = 0x540;            // and key norm
-  static constexpr uint32_t VOWN = 0x600;            // the same as VMAX, for the V-filling warps alone
   static constexpr uint32_t NK = 0x800, NV = 0x1000; // [4 tiles][TN] norms
   static constexpr uint32_t PT = 0x2000;             // few rows: weights [2 tiles][2 × 64 tokens][16 rows], swizzled
   static constexpr uint32_t QB = 0x4000;             // few rows: queries [part][64 coordinates][16 rows], swizzled
@@ -211,12 +207,10 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-// A shared word that later copies overwrite (lds_u32 is for constant tables).
-__device__ __forceinline__ uint32_t lds_code(uint32_t addr, int bytes) {
+// A shared word that is written again later (lds_u32 is for constant tables).
+__device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
   uint32_t v;
-  if (bytes == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-  else if (bytes == 2) asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(addr));
-  else asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 
@@ -233,7 +227,7 @@ template <int D, int B> __device__ __forceinline__ void read_octets(uint32_t pie
     w[0] = v.x, w[1] = v.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < B; ++i) w[i] = lds_code(piece + code_at<PITCH>(r, off + 4 * i), 4);
+    for (int i = 0; i < B; ++i) w[i] = lds_word(piece + code_at<PITCH>(r, off + 4 * i));
   }
 }
 // Octet i of four, as nibbles.
@@ -244,12 +238,7 @@ template <int B> __device__ __forceinline__ uint32_t octet_of(const uint32_t (&w
   if (sh + 8 * B > 32) v = __funnelshift_r(w[k], w[k + 1 < 4 ? k + 1 : 3], sh);
   return octet_nibbles(v & (B == 3 ? 0xffffffu : B == 2 ? 0xffffu : 0xffu), B);
 }
-template <bool SCALE> __device__ __forceinline__ uint32_t times(uint32_t pair, __half2 nu) {
-  if constexpr (!SCALE) return pair;
-  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&pair), nu);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-// The largest of a tile's norms, as the K-filling warps left them.
+// The largest of a tile's value norms, as the K-filling warps left them.
 template <int TN> __device__ __forceinline__ float tile_max(uint32_t at, int j) {
   const float4 m = lds_f4(at + uint32_t(j & 3) * 16);
   return TN == 128 ? fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) : fmaxf(m.x, m.y);
@@ -259,10 +248,9 @@ template <int K> __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_
   return lds_u32(__byte_perm(w, lane_word, K == 0 ? 0x7604u : K == 1 ? 0x7614u : K == 2 ? 0x7624u : 0x7634u));
 }
 
-// Four octets of a token's row as levels, chunks c0 .. c0 + 3 of `row`; SCALE: times `nu`.  All
+// Four octets of a token's row as levels, chunks c0 .. c0 + 3 of `row`.  All
 // lookups come before the first store: a load is not moved ahead of a store that might alias it.
-template <int B, bool SCALE>
-__device__ __forceinline__ void put_octets(const uint32_t (&w)[4], uint32_t row, int c0, int n, uint32_t lane_word, __half2 nu) {
+template <int B> __device__ __forceinline__ void put_octets(const uint32_t (&w)[4], uint32_t row, int c0, int n, uint32_t lane_word) {
   uint32_t p[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -272,8 +260,7 @@ __device__ __forceinline__ void put_octets(const uint32_t (&w)[4], uint32_t row,
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    sts_v4(row + (uint32_t((c0 + i) ^ (n & 7)) << 4), times<SCALE>(p[i][0], nu), times<SCALE>(p[i][1], nu),
-           times<SCALE>(p[i][2], nu), times<SCALE>(p[i][3], nu));
+    sts_v4(row + (uint32_t((c0 + i) ^ (n & 7)) << 4), p[i][0], p[i][1], p[i][2], p[i][3]);
 }
 
 // Columns [h, h + 32) of a tile: `v` where the column's token is not one of the first `valid`.
@@ -308,10 +295,11 @@ struct Cursor {
   }
 };
 
-template <int D, bool SPLIT, bool FOLD>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ SharedMaps maps) {
   using L = Tc<D>;
   constexpr int TN = L::TN;
+  constexpr bool SPLIT = D <= 128;
   extern __shared__ __align__(1024) uint8_t dsm[];
   pdl_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -324,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   auto s_full = [&](int j) { return &bars[5 + (j & 1)]; };
   auto p_full = [&](int j) { return &bars[7 + (j & 1)]; };
   auto o_done = [&](int j) { return &bars[9 + (j & 1)]; };
-  auto c_full = [&](int j) { return &bars[12 + (j & 1)]; };
-  auto c_free = [&](int j) { return &bars[14 + (j & 1)]; };
+  auto c_full = [&](int j, bool v) { return &bars[(v ? 17 : 12) + (j & 1)]; };
+  auto c_free = [&](int j, bool v) { return &bars[(v ? 19 : 14) + (j & 1)]; };
   auto phase = [](int j) { return uint32_t(j >> 1) & 1u; };
   uint32_t* tslot = reinterpret_cast<uint32_t*>(at(L::TSLOT));
   volatile int* fail = reinterpret_cast<volatile int*>(at(L::FAIL));
@@ -339,8 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), kSoftWarps);
       mbar_init(o_done(s), 1);
-      mbar_init(c_full(s), 1);
-      mbar_init(c_free(s), kFillWarps);
+      for (int v = 0; v < 2; ++v) {
+        mbar_init(c_full(s, v), 1);
+        mbar_init(c_free(s, v), kFillWarps / 2);
+      }
     }
     *fail = placed ? 0 : 1;
     fence_mbarrier_init();
@@ -428,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               if (ok) {
                 uint32_t v[8];
                 tmem_ld8(tl + uint32_t(L::S + (j & 1) * TN + 8 * half), v);
-                const float nk = __uint_as_float(lds_code(L::NK + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4, 4));
-                nv = __uint_as_float(lds_code(L::NV + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4, 4));
+                const float nk = __uint_as_float(lds_word(L::NK + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4));
+                nv = __uint_as_float(lds_word(L::NV + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4));
                 tmem_ld_wait();
                 if (i == 0) {
                   const float4 r0 = lds_f4(L::RS + uint32_t(seg & 1) * 64 + uint32_t(half) * 32);
@@ -509,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           // the next segment's queries go in while this one's last product runs: S of all its
           // tiles is done
           c.next_segment(a);
-          if (c.live()) {  // tails behind a prefix of few rows have no more rows than it
+          if (c.live() && c.s.nrows <= kFewRows) {
             stage(c.s, seg + 1);
             staged = true;
           }
@@ -531,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             if (quarter == 0 && lane < 8 && 8 * half + lane < s.nrows) {
               float sum = 0.f, mine_mp = mp[0];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) sum += __uint_as_float(lds_code(wl + uint32_t(q) * 32 + uint32_t(lane) * 4, 4));
+              for (int q = 0; q < 4; ++q) sum += __uint_as_float(lds_word(wl + uint32_t(q) * 32 + uint32_t(lane) * 4));
 #pragma unroll
               for (int r = 1; r < 8; ++r)
                 if (lane == r) mine_mp = mp[r];
@@ -606,11 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                   for (int k = 0; k < 32; k += 4) {
                     y[k / 2] = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
                     y[k / 2 + 1] = make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-                    if constexpr (!FOLD) {
-                      const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
-                      y[k / 2] = mul2(y[k / 2], make_float2(n.x, n.y));
-                      y[k / 2 + 1] = mul2(y[k / 2 + 1], make_float2(n.z, n.w));
-                    }
+                    const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
+                    y[k / 2] = mul2(y[k / 2], make_float2(n.x, n.y));
+                    y[k / 2 + 1] = mul2(y[k / 2 + 1], make_float2(n.z, n.w));
                   }
                   if constexpr (!decltype(whole)::value) mask(y, half * TH + h, valid, -INFINITY);
 #pragma unroll
@@ -623,9 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             }
             ok = meet(pair, 64, ok);
             if (ok) {
-              // 2^e, times the unit of the tile's key norms where these are in K already
-              const float rj = FOLD ? rs * norm_unit(tile_max<TN>(L::KMAX, j)) : rs;
-              mx = fmaxf(mx, __uint_as_float(lds_code(xch + uint32_t(half ^ 1) * 512, 4))) * rj;
+              mx = fmaxf(mx, __uint_as_float(lds_word(xch + uint32_t(half ^ 1) * 512))) * rs;
               const float pw = norm_unit(tile_max<TN>(L::VMAX, j));
               if (i == 0) {
                 m = mx;
@@ -653,10 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                   tmem_st_wait();
                 }
               }
-              // weights into S's columns, the sum of the exponentials; with the value norms (over
-              // their unit pw) in V already, the weights carry pw and the sum is freed of it
-              const float mj = FOLD ? mp - float(int(__float_as_uint(pw) >> 23) - 127) : mp;
-              const float2 rs2 = make_float2(rj, rj), mp2 = make_float2(-mj, -mj);
+              // weights into S's columns, the sum of the exponentials
+              const float2 rs2 = make_float2(rs, rs), mp2 = make_float2(-mp, -mp);
               const uint32_t pb = sb;  // the first half of the columns that this thread reads
               float2 s2 = make_float2(0.f, 0.f), s3 = s2;
               auto weigh = [&](auto whole) {
@@ -670,11 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                   for (int k = 0; k < 32; k += 4) {
                     float2 x0 = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
                     float2 x1 = make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-                    if constexpr (!FOLD) {
-                      const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
-                      x0 = mul2(x0, make_float2(n.x, n.y));
-                      x1 = mul2(x1, make_float2(n.z, n.w));
-                    }
+                    const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
+                    x0 = mul2(x0, make_float2(n.x, n.y));
+                    x1 = mul2(x1, make_float2(n.z, n.w));
                     x0 = fma2(x0, rs2, mp2);
                     x1 = fma2(x1, rs2, mp2);
                     e[k / 2] = make_float2(ex2(x0.x), ex2(x0.y));
@@ -686,11 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                     float2 w0 = e[k / 2], w1 = e[k / 2 + 1];
                     s2 = add2(s2, w0);
                     s3 = add2(s3, w1);
-                    if constexpr (!FOLD) {
-                      const float4 w = lds_f4(nv + uint32_t(h + k) * 4);
-                      w0 = mul2(w0, make_float2(w.x, w.y));
-                      w1 = mul2(w1, make_float2(w.z, w.w));
-                    }
+                    const float4 w = lds_f4(nv + uint32_t(h + k) * 4);
+                    w0 = mul2(w0, make_float2(w.x, w.y));
+                    w1 = mul2(w1, make_float2(w.z, w.w));
                     const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
                     p[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
                     p[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
@@ -700,8 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               };
               if (full) weigh(std::true_type{});
               else weigh(std::false_type{});
-              const float u = FOLD ? 1.f / pw : 1.f;  // a power of two
-              l += u * ((s2.x + s2.y) + (s3.x + s3.y));
+              l += (s2.x + s2.y) + (s3.x + s3.y);
               tmem_st_wait();
             }
           }
@@ -719,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           ok = meet(pair, 64, ok);
           const int64_t st = int64_t(s.state) * a.rows + s.row0 + ln;
           if (!half && row_ok)
-            a.stats[st] = ok ? make_float2(mp, l + __uint_as_float(lds_code(xch, 4))) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
+            a.stats[st] = ok ? make_float2(mp, l + __uint_as_float(lds_word(xch))) : make_float2(__uint_as_float(0x7fc00000u), 0.f);
           if (ok) {
 #pragma unroll 1
             for (int k = 0; k < DH; k += 32) {
@@ -744,23 +723,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     }
   } else if (warp < kSoftWarps + kFillWarps) {
     // ------------------------------------------------------------ codes to fp16 levels in shared memory
-    // Four warps for K, four for V, the same code; the K side also leaves both norms for the weights.
+    // Four warps for K, four for V, the same code; the K side also leaves the norms for the weights.
     const bool v_side = warp >= kSoftWarps + kFillWarps / 2;
     const int ft = (tid - kSoftWarps * 32) & (kFill - 1);
     const int n = ft % TN, sub = ft / TN;  // row of the tile
     const int tok = token_of(n);
     const int bits = v_side ? a.v_bits : a.k_bits;
     const uint32_t lane_word = L::TABLE | uint32_t(lane * 4) | (v_side ? 128u : 0u);
-    const uint32_t piece0 = L::piece(0, v_side, tok / L::PR), maxima = v_side ? L::VOWN : L::KMAX;
+    const uint32_t piece0 = L::piece(0, v_side, tok / L::PR);
     Cursor c(a, range);
     uint32_t kw[2][4];  // rows that no box moves (d = 64)
-    float norm = 0.f, norm_v = 0.f;
+    float norm_k = 0.f, norm_v = 0.f;
     auto fetch = [&] {  // what comes from global memory for the cursor's tile; rows past the end repeat the last
       const int tt = c.i * TN + tok, part = c.s.flags & 1;
       const bool in = tt < c.s.tokens;
       const int64_t row = int64_t(c.s.token + (in ? tt : c.s.tokens - 1)) * a.hkv + c.s.g;
-      norm_v = in ? __ldg(a.v_norms[part] + row) : 0.f;
-      norm = v_side ? norm_v : __ldg(a.k_norms[part] + row);
+      if (!v_side) {
+        norm_k = __ldg(a.k_norms[part] + row);
+        norm_v = in ? __ldg(a.v_norms[part] + row) : 0.f;
+      }
       if constexpr (D == 64) {
         if (bits & 1) {
           const uint32_t* p = reinterpret_cast<const uint32_t*>((v_side ? a.v_codes : a.k_codes)[part] + row * (D * bits / 8));
@@ -777,28 +758,32 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     for (int j = 0; c.live(); ++j) {
       // the codes are there; K's stage has been read by S of the last tile but one, V's tile by
       // O of the last
-      ok = ok && wait_for(c_full(j), phase(j), fail);
+      ok = ok && wait_for(c_full(j, v_side), phase(j), fail);
       if (v_side) ok = ok && (j < 1 || wait_for(o_done(j - 1), phase(j - 1), fail));
       else ok = ok && (j < 2 || wait_for(s_full(j), phase(j - 2), fail));
-      // norm slots are used every fourth tile: what read this one before was done when S of
-      // tile j − 2 began
-      const float big = warp_max(fabsf(norm));
-      if (!v_side) {
+      if (!v_side && sub == 0) {
+        // norm slots are used every fourth tile: what read this one before was done when S of
+        // tile j − 2 began
         const uint32_t slot = uint32_t(j & 3) * (TN * 4) + uint32_t(n) * 4;
-        const float vmax = warp_max(fabsf(norm_v));
-        if (sub == 0) {
-          *reinterpret_cast<float*>(at(L::NK + slot)) = norm;
-          *reinterpret_cast<float*>(at(L::NV + slot)) = norm_v;
-          if (lane == 0) *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = vmax;
-        }
+        *reinterpret_cast<float*>(at(L::NK + slot)) = norm_k;
+        *reinterpret_cast<float*>(at(L::NV + slot)) = norm_v;
+        const float big = warp_max(fabsf(norm_v));
+        if (lane == 0) *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = big;
       }
-      if (sub == 0 && lane == 0) *reinterpret_cast<float*>(at(maxima + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = big;
-      ok = meet(v_side ? 8 : 7, kFill, ok);
+      ok = __all_sync(kFull, ok);
       if (!ok) break;
-      const bool fold = FOLD && !(D <= 128 && c.s.nrows <= kFewRows);
-      const __half2 nu = __float2half2_rn(fold ? norm / norm_unit(tile_max<TN>(maxima, j)) : 1.f);
       const uint32_t dst = (v_side ? L::VT : L::K0 + uint32_t(j & 1) * 0x8000u) + uint32_t(n) * 128;
       const uint32_t piece = piece0 + uint32_t(j & 1) * 0x4000u;
+      uint32_t cw[2][4];
+      if constexpr (D == 64) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 3; ++k) cw[i][k] = kw[i][k];
+      }
+      // the next tile's norms are on their way while this one is filled
+      c.next(a);
+      if (c.live()) fetch();
       auto fill = [&](auto width) {
         constexpr int B = decltype(width)::value;
         if constexpr (kBoxed<D, B>) {
@@ -806,11 +791,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           for (int it = sub * L::TURNS; it < (sub + 1) * L::TURNS; ++it) {
             uint32_t w[4];
             read_octets<D, B>(piece, tok % L::PR, it, w);
-            put_octets<B, FOLD>(w, dst + uint32_t(it >> 1) * (TN * 128), (it & 1) * 4, n, lane_word, nu);
+            put_octets<B>(w, dst + uint32_t(it >> 1) * (TN * 128), (it & 1) * 4, n, lane_word);
           }
         } else {
-          put_octets<B, FOLD>(kw[0], dst, 0, n, lane_word, nu);
-          put_octets<B, FOLD>(kw[1], dst, 4, n, lane_word, nu);
+          put_octets<B>(cw[0], dst, 0, n, lane_word);
+          put_octets<B>(cw[1], dst, 4, n, lane_word);
         }
       };
       switch (bits) {
@@ -823,36 +808,45 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(v_side ? v_full(j) : k_full(j));
-        mbar_arrive(c_free(j));
+        mbar_arrive(c_free(j, v_side));
       }
-      c.next(a);
-      if (c.live()) fetch();
     }
   } else if (warp == kSoftWarps + kFillWarps + 1) {
     // ---------------------------------------------------------------- one thread copies the packed codes
     if (lane == 0) {
       const bool kbox = D * a.k_bits / 8 % 16 == 0, vbox = D * a.v_bits / 8 % 16 == 0;
       const int krow = D * a.k_bits / 8, vrow = D * a.v_bits / 8;
-      const uint32_t bytes = (kbox ? TN * krow : 0) + (vbox ? TN * vrow : 0);
-      bool ok = placed;
-      int j = 0;
-      for (Cursor c(a, range); c.live(); c.next(a), ++j) {
-        if (j >= 2) ok = ok && wait_for(c_free(j), phase(j - 2), fail);
-        if (!ok) break;
-        const uint32_t bar = smem_addr(c_full(j));
-        mbarrier_expect_tx(bar, bytes);
-        const int t = c.s.token + c.i * TN, part = c.s.flags & 1;
+      // K a tile ahead of V, as the filling warps take them
+      Cursor ck(a, range), cv = ck;
+      int jk = 0, jv = 0;
+      auto copy = [&](Cursor& c, int& j, bool v) {
+        const int row = v ? vrow : krow;
+        const bool box = v ? vbox : kbox;
+        if (j >= 2 && !wait_for(c_free(j, v), phase(j - 2), fail)) return false;
+        const uint32_t bar = smem_addr(c_full(j, v));
+        mbarrier_expect_tx(bar, box ? uint32_t(TN * row) : 0u);
+        const CUtensorMap* map = (v ? maps.v : maps.k) + (c.s.flags & 1);
+        if (box) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int y = t + h * L::PR;  // rows past the cache's end are filled with zeros
-          if (kbox) tma_load_2d(L::piece(j & 1, 0, h), &maps.k[part], c.s.g * krow, y, bar);
-          if (vbox) tma_load_2d(L::piece(j & 1, 1, h), &maps.v[part], c.s.g * vrow, y, bar);
+          for (int h = 0; h < 2; ++h)  // rows past the cache's end are filled with zeros
+            tma_load_2d(L::piece(j & 1, v, h), map, c.s.g * row, c.s.token + c.i * TN + h * L::PR, bar);
         }
+        c.next(a);
+        ++j;
+        return true;
+      };
+      bool ok = placed;
+      while (ok && cv.live()) {
+        if (ck.live()) ok = copy(ck, jk, false);
+        if (ok && (jv + 1 < jk || !ck.live())) ok = copy(cv, jv, true);
       }
       // copies still in flight end before the CTA does
-      for (int k = j > 2 ? j - 2 : 0; k < j; ++k)
-        for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(c_full(k), phase(k)); ++i) {
-        }
+      for (int v = 0; v < 2; ++v) {
+        const int n = v ? jv : jk;
+        for (int k = n > 2 ? n - 2 : 0; k < n; ++k)
+          for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(c_full(k, v), phase(k)); ++i) {
+          }
+      }
     }
   } else {
     // ---------------------------------------------------------------- products; the warps stay together, one thread issues
@@ -939,8 +933,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   }
 }
 
-template <int D, bool SPLIT, bool FOLD> cudaError_t launch_split(const SharedArgs& a, cudaStream_t stream) {
-  auto k = shared_tc_kernel<D, SPLIT, FOLD>;
+template <int D> cudaError_t launch_tc(const SharedArgs& a, cudaStream_t stream) {
+  auto k = shared_tc_kernel<D>;
   static std::atomic<uint64_t> done;
   const cudaError_t e = allow_kernel(k, int(Tc<D>::kTotal), &done);
   if (e != cudaSuccess) return e;
@@ -967,10 +961,8 @@ cudaError_t launch_shared_tc(const SharedArgs& a, cudaStream_t stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
   if (e != cudaSuccess) return e;
   if (uint32_t(reserved) != Tc<128>::kBase) return cudaErrorNotSupported;
-  // bf16: what the norms lose in fp16 operands is far below a step of the output
-  if (a.d == 64) return a.split ? launch_split<64, true, false>(a, stream) : launch_split<64, false, true>(a, stream);
-  if (a.d == 128) return a.split ? launch_split<128, true, false>(a, stream) : launch_split<128, false, true>(a, stream);
-  return a.bf16 ? launch_split<256, false, true>(a, stream) : launch_split<256, false, false>(a, stream);
+  if (a.d == 64) return launch_tc<64>(a, stream);
+  return a.d == 128 ? launch_tc<128>(a, stream) : launch_tc<256>(a, stream);
 }
 
 }  // namespace rrq

@@ -184,6 +184,19 @@ def test_attention_shared_long_prefix_many_rows():
     assert np.all(err <= 2e-3 * weight + 2.0 ** -8 * np.linalg.norm(ref, axis=2))
 
 
+@pytest.mark.parametrize("d,dtype", [(128, torch.float16), (128, torch.bfloat16), (64, torch.float16)])
+@pytest.mark.parametrize("batch,cap", [(65, 0), (70, 40)])
+def test_attention_shared_few_rows_before_many(d, dtype, batch, cap):
+    """130 or 140 rows per kv head leave a last tile of 2 or 12 rows, and some ranges go on from
+    it to the next head's 128 rows."""
+    rg = np.random.Generator(np.random.PCG64(batch + d))
+    hkv, prefix = 4, 6400
+    p = _part(rg, prefix * hkv, d, 4, 4)
+    t = _part(rg, batch * cap * hkv, d, 4, 4) if cap else None
+    q = rg.standard_normal((batch, 2 * hkv, d))
+    _check_attention(q, p, t, rg.integers(0, cap + 1, size=batch), hkv, d, 4, 4, d ** -0.5, dtype, f"{batch} x 2 rows, d {d}")
+
+
 def test_attention_shared_is_decode_attention_for_one_sequence():
     """The same cache through rrq_attention_decode: both within the bound of the exact one."""
     rg = np.random.Generator(np.random.PCG64(14))
