@@ -343,9 +343,11 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  * Alignment: codes, q and out 16 bytes, norms and tail_lens 4.
  * Accuracy: softmax statistics, sums and the rotations in fp32.  For d ≤ 256 both
  * products run on the tensor cores with fp16 operands and fp32 sums; value weights
- * are scaled so that value norms within 2^-20 of the largest one keep their precision.
- * Per head the output is within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is
- * rounded to q_dtype.
+ * are scaled so that value norms within 2^-18 of the largest one keep their precision.
+ * The rotated queries are two fp16 parts (22 bits) for d ≤ 128 and one (11 bits, a
+ * score's error up to 2^-11·scale·‖q‖·‖k̂_t‖ and on average √d times smaller) for d = 256.
+ * For d ≠ 256, and for d = 256 while the scores' own error stays below 5e-4, the output
+ * of a head is within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is rounded to q_dtype.
  * Errors: RRQ_ERR_INVALID (incl. a workspace that is too small), RRQ_ERR_UNSUPPORTED
  * (q_dtype RRQ_F32, more than 128 heads per kv head, 2^31 − 128 or more tokens in the
  * prefix or over all tails, 10^8 or more tiles of 64 or 128 tokens over all units of work,

@@ -7,10 +7,10 @@
 // memory has no room for) and the levels c as fp16,
 //     S = Q'·C_Kᵀ,   x = 2^e·ν^K_t·S,   P = 2^{x − m'}·ν^V_t,   O += P·C_V,
 // where m' follows the row's running maximum m: it moves only when m grows by more than
-// 4 (powers of two), so O is rarely rescaled, and it carries the power of two that
+// 8 (powers of two), so O is rarely rescaled, and it carries the power of two that
 // brings the weights into fp16's range: with N the power of two below the largest ν^V
-// seen (it moves when that grows fourfold), m' = m − 8 + log2 N, so weights are at most
-// 2^15 and keep full precision down to 2^-22 of the largest.  The state (m', Σ 2^{x − m'}, O)
+// seen (it moves when that grows fourfold), m' = m − 4 + log2 N, so weights are at most
+// 2^15 and keep full precision down to 2^-18 of the largest.  The state (m', Σ 2^{x − m'}, O)
 // is what the merge takes.
 //
 // Units of at most 16 rows (d ≤ 128) exchange the operands' roles: a tile's 128 tokens are the
@@ -47,6 +47,7 @@ namespace {
 constexpr uint32_t kWaitLimit = 1u << 24;  // polls, a few seconds in all
 constexpr int kSoftWarps = 8, kFillWarps = 8;
 constexpr int kFill = 128;  // threads that fill K, and as many that fill V
+constexpr float kGrowth = 8.f, kRoom = 4.f;  // of a row's maximum before m' moves; of the weights above it
 constexpr int kFewRows = 16;  // rows of a unit that exchanges the operands' roles
 constexpr int kThreads = (kSoftWarps + kFillWarps + 3) * 32;
 
@@ -173,7 +174,7 @@ __device__ __forceinline__ float norm_unit(float big) {
 }
 // m' of a running maximum m and the unit N: weights 2^{x − m'}·ν are at most 2^15.
 __device__ __forceinline__ float shifted(float m, float unit) {
-  return m - 8.f + float(int(__float_as_uint(unit) >> 23) - 127);
+  return m - kRoom + float(int(__float_as_uint(unit) >> 23) - 127);
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                   const bool wide = pw > 4.f * vn;
                   bool up = wide;
 #pragma unroll
-                  for (int r = 0; r < 8; ++r) up = up || mx[r] * rs[r] > m[r] + 4.f;
+                  for (int r = 0; r < 8; ++r) up = up || mx[r] * rs[r] > m[r] + kGrowth;
                   if (up) {  // the same in every thread of the half
                     if (wide) vn = pw;
                     ok = __all_sync(kFull, wait_for(o_done(j - 1), phase(j - 1), fail));
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                     tmem_ld_wait();
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                      if (mx[r] * rs[r] > m[r] + 4.f) m[r] = mx[r] * rs[r];
+                      if (mx[r] * rs[r] > m[r] + kGrowth) m[r] = mx[r] * rs[r];
                       const float mn = shifted(m[r], vn), f = ex2(mp[r] - mn);
                       mp[r] = mn;
                       l[r] *= f;
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                 vn = pw;
                 mp = shifted(m, vn);
               } else {
-                const bool up = mx > m + 4.f, wide = pw > 4.f * vn;
+                const bool up = mx > m + kGrowth, wide = pw > 4.f * vn;
                 if (__any_sync(kFull, up || wide)) {
                   if (up) m = mx;
                   if (wide) vn = pw;
