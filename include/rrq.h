@@ -387,10 +387,11 @@ size_t rrq_attention_shared_workspace_bytes(int64_t batch, int hq, int hkv, int 
  *           [0, T] count as the nearer end
  *   mass    [batch × hkv × T] float, or NULL (zeros);  out may be the same array
  *   out     [batch × hkv × T] float (output)
- * hq a multiple of hkv.  batch = 0 or T = 0 is a no-op.  T < 2^31.  Arrays 4-byte
- * aligned (16-byte vectors are used where addresses and T allow).  fp32 throughout;
+ * hq a multiple of hkv, at most 1024 query heads per kv head.  batch = 0 or T = 0 is a
+ * no-op.  T < 2^31, batch·hkv ≤ 2^27.  Arrays 4-byte aligned (16-byte vectors are used where addresses and T allow).  fp32 throughout;
  * the result does not depend on the order in which the GPU runs blocks.
- * Errors: RRQ_ERR_INVALID (incl. a decay that is not finite), RRQ_ERR_CUDA.
+ * Errors: RRQ_ERR_INVALID (incl. a decay that is not finite), RRQ_ERR_UNSUPPORTED (more
+ * than 1024 query heads per kv head), RRQ_ERR_CUDA.
  */
 int rrq_attention_mass(const float* scores, int64_t batch, int hq, int hkv, int64_t T,
                        const int32_t* lens, float decay, const float* mass, float* out,
@@ -416,7 +417,7 @@ int rrq_attention_mass(const float* scores, int64_t batch, int hq, int hkv, int6
  *   out_mass  [batch × hkv × keep] float, or NULL;
  *   ok_codes, ok_norms, ov_codes, ov_norms: the output cache of capacity keep
  * Inputs and outputs must not overlap.  keep ≥ 1, sink, recent ≥ 0 with
- * sink + recent ≤ keep; cap < 2^31.  batch = 0 or cap = 0: out_lens is set to 0 for
+ * sink + recent ≤ keep; cap < 2^31, batch·hkv ≤ 2^27.  batch = 0 or cap = 0: out_lens is set to 0 for
  * every sequence, nothing else is written.  Alignment: codes 16 bytes, the rest 4.
  * Errors: RRQ_ERR_INVALID, RRQ_ERR_CUDA.
  */

@@ -482,11 +482,13 @@ int rrq_attention_shared(const void* q, int q_dtype, int64_t batch, int hq,
   a.k_seed = k_seed;
   a.v_seed = v_seed;
   a.kscale = static_cast<float>(double(scale) * 1.4426950408889634074 / d);
-  // fp16 queries: a second fp16 part keeps what the rotation would lose; bf16 ones have less to lose
   rrq::attention_shared_levels(&a, k_codebook == nullptr, v_codebook == nullptr);
   const cudaError_t e = rrq::launch_attention_shared(a, as_stream(stream));
   return e == cudaErrorNotSupported ? RRQ_ERR_UNSUPPORTED : status_of(e);
 }
+
+// Sequences × kv heads of the two calls below: a cluster of up to 16 blocks each in one grid.
+constexpr int kMaxRows = 1 << 27;
 
 int rrq_attention_mass(const float* scores, int64_t batch, int hq, int hkv, int64_t T,
                        const int32_t* lens, float decay, const float* mass, float* out,
@@ -496,7 +498,8 @@ int rrq_attention_mass(const float* scores, int64_t batch, int hq, int hkv, int6
   const int64_t n = batch > 0 ? T : 0;
   if (!arr_ok(scores, n, 4) || !aligned(lens, 4) || !aligned(mass, 4) || !arr_ok(out, n, 4))
     return RRQ_ERR_INVALID;
-  if (batch > INT32_MAX / hkv) return RRQ_ERR_INVALID;
+  if (batch > kMaxRows / hkv) return RRQ_ERR_INVALID;
+  if (hq / hkv > rrq::kMassHeads) return RRQ_ERR_UNSUPPORTED;
   if (n == 0) return RRQ_OK;
   rrq::MassArgs a;
   a.scores = scores;
@@ -528,7 +531,7 @@ int rrq_evict(const float* mass, int64_t batch, int hkv, int64_t cap, const int3
       !arr_ok(ok_codes, n, 16) || !arr_ok(ok_norms, n, 4) || !arr_ok(ov_codes, n, 16) ||
       !arr_ok(ov_norms, n, 4))
     return RRQ_ERR_INVALID;
-  if (batch > INT32_MAX / hkv) return RRQ_ERR_INVALID;
+  if (batch > kMaxRows / hkv) return RRQ_ERR_INVALID;
   if (batch == 0) return RRQ_OK;
   if (cap == 0) return status_of(cudaMemsetAsync(out_lens, 0, size_t(batch) * 4, as_stream(stream)));
   rrq::EvictArgs a;

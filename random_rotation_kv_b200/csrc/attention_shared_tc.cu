@@ -735,13 +735,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     Cursor c(a, range);
     uint32_t kw[2][4];  // rows that no box moves (d = 64)
     float norm_k = 0.f, norm_v = 0.f;
-    auto fetch = [&] {  // what comes from global memory for the cursor's tile; rows past the end repeat the last
+    // what comes from global memory for the cursor's tile; rows past the end repeat the last (not
+    // through L1: the launch that wrote them may still have run when this one began)
+    auto fetch = [&] {
       const int tt = c.i * TN + tok, part = c.s.flags & 1;
       const bool in = tt < c.s.tokens;
       const int64_t row = int64_t(c.s.token + (in ? tt : c.s.tokens - 1)) * a.hkv + c.s.g;
       if (!v_side) {
-        norm_k = __ldg(a.k_norms[part] + row);
-        norm_v = in ? __ldg(a.v_norms[part] + row) : 0.f;
+        norm_k = __ldcg(a.k_norms[part] + row);
+        norm_v = in ? __ldcg(a.v_norms[part] + row) : 0.f;
       }
       if constexpr (D == 64) {
         if (bits & 1) {
@@ -750,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int k = 0; k < 3; ++k)
-              if (k < bits) kw[i][k] = __ldg(p + i * bits + k);
+              if (k < bits) kw[i][k] = __ldcg(p + i * bits + k);
         }
       }
     };

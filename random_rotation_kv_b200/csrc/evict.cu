@@ -12,6 +12,8 @@
 // counts' prefixes give each kept token its slot, and of the equal ones the first are
 // kept; so the order of blocks and atomics never shows in the result.  The passes are bound
 // by their four cluster barriers, not by the masses, which are read once.
+// Loads of what another launch may have written bypass L1 (also in mass.cu): launches overlap,
+// so this kernel may have begun before that one ended.
 // Moving: a second launch over all SMs copies the rows, 128 per block, 16 bytes (8 where rows
 // are not a multiple of 16) per access with the code rows of the new cache written in
 // one run; it is bound by memory (2·(d·(kb + vb)/8 + 8) bytes per kept row).
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int t = base + first + 32 * i;
-      v[i] = t < mine ? __ldg(mass + t) : 0.f;
+      v[i] = t < mine ? __ldcg(mass + t) : 0.f;
     }
   };
   auto key_of = [&](int base, int i) {
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
       if (tid < live) {
         const int64_t s = (r0 + tid) / a.hkv;
         const int64_t g = (r0 + tid) - s * a.hkv;
-        s_src[tid] = (b * a.cap + __ldg(a.index + (b * a.hkv + g) * a.keep + s)) * a.hkv + g;
+        s_src[tid] = (b * a.cap + __ldcg(a.index + (b * a.hkv + g) * a.keep + s)) * a.hkv + g;
       }
       __syncthreads();
       const int64_t to = b * a.keep * a.hkv + r0;
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const unsigned i = unsigned(i0 + e * kMoveThreads);
-            if (int(i) < total) w[e] = __ldg(f + s_src[i / unsigned(units)] * units + i % unsigned(units));
+            if (int(i) < total) w[e] = __ldcg(f + s_src[i / unsigned(units)] * units + i % unsigned(units));
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
       };
       float nu = 0.f;
       const int r = tid & (kMoveRows - 1);
-      if (r < live) nu = __ldg((tid < kMoveRows ? a.k_norms : a.v_norms) + s_src[r]);
+      if (r < live) nu = __ldcg((tid < kMoveRows ? a.k_norms : a.v_norms) + s_src[r]);
       copy(a.k_codes, a.ok_codes, ku);
       copy(a.v_codes, a.ov_codes, vu);
       if (r < live) (tid < kMoveRows ? a.ok_norms : a.ov_norms)[to + r] = nu;

@@ -7,6 +7,8 @@
 
 namespace rrq {
 
+constexpr int kMassHeads = 1024;  // query heads per kv head
+
 struct MassArgs {
   const float* scores;  // [batch × hq × T]
   const int32_t* lens;  // [batch] or null

@@ -21,7 +21,6 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr size_t kMaxScores = 218 * 1024;  // bytes of scores and maxima a CTA keeps
 constexpr size_t kMaxSmem = 224 * 1024;
 
 __device__ __forceinline__ int64_t clamp_len(const int32_t* lens, int64_t b, int64_t cap) {
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const MassArgs a, int ch
       for (int t = tid; t < mine; t += kThreads) {
         float v[kHeads];
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) v[h] = h < hs ? __ldg(s + int64_t(h) * a.T + t) : -INFINITY;
+        for (int h = 0; h < kHeads; ++h) v[h] = h < hs ? __ldcg(s + int64_t(h) * a.T + t) : -INFINITY;
 #pragma unroll
         for (int h = 0; h < kHeads; ++h) {
           if constexpr (KEEP)
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const MassArgs a, int ch
 #pragma unroll
         for (int h = 0; h < kHeads; ++h)
           if (h < hs) {
-            const float v = KEEP ? k[int64_t(h) * chunk + t] : __ldg(s + int64_t(h) * a.T + t);
+            const float v = KEEP ? k[int64_t(h) * chunk + t] : __ldcg(s + int64_t(h) * a.T + t);
             const float e = m[h] != -INFINITY ? exp2_approx((v - m[h]) * kLog2e) : 0.f;
             if constexpr (KEEP) k[int64_t(h) * chunk + t] = e;
             l[h] += e;
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const MassArgs a, int ch
           w = fmaf(s_keep[int64_t(h) * chunk + t], s_mt[h * kThreads + tid], w);
         } else {
           const float m = s_f[2 * h];
-          if (m != -INFINITY) w = fmaf(exp2_approx((__ldg(sc + int64_t(h) * a.T + t) - m) * kLog2e), s_f[2 * h + 1], w);
+          if (m != -INFINITY) w = fmaf(exp2_approx((__ldcg(sc + int64_t(h) * a.T + t) - m) * kLog2e), s_f[2 * h + 1], w);
         }
       }
       out[t] = fmaf(a.decay, in ? in[t] : 0.f, w);
@@ -259,18 +258,18 @@ cudaError_t launch_attention_mass(const MassArgs& a, cudaStream_t stream) {
   const int64_t rows = a.batch * a.hkv;
   unsigned size = cluster_size(rows, a.T, 512);
   auto share = [&](unsigned c) { return ((a.T + c - 1) / c + 3) / 4 * 4; };
-  auto bytes = [&](unsigned c) { return (size_t(share(c)) + kThreads) * a.group * 4; };
+  const size_t pairs = size_t(a.group) * (16 + kWarps * 8);
+  auto bytes = [&](unsigned c) { return (size_t(share(c)) + kThreads) * a.group * 4 + pairs; };  // with the scores kept
   // Runs whose scores take more than half of an SM's shared memory leave one CTA per SM.
   // Of clusters above 10 only 7 then run at a time (15 of 9, 11 of 10: the SMs of a GPC),
   // so 10 is tried before 16.
-  while (size < 8 && bytes(size) > kMaxScores) size *= 2;
-  if (bytes(size) > kMaxScores || (size == 16 && bytes(16) > 100 * 1024)) size = bytes(10) <= kMaxScores ? 10 : 16;
+  while (size < 8 && bytes(size) > kMaxSmem) size *= 2;
+  if (bytes(size) > kMaxSmem || (size == 16 && bytes(16) > 100 * 1024)) size = bytes(10) <= kMaxSmem ? 10 : 16;
   const int64_t chunk = share(size);
-  const bool keep = bytes(size) <= kMaxScores;
+  const bool keep = bytes(size) <= kMaxSmem;
   const bool vec = a.T % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scores) | reinterpret_cast<uintptr_t>(a.mass) |
                                     reinterpret_cast<uintptr_t>(a.out)) % 16 == 0;
-  const size_t smem = (keep ? bytes(size) : 0) + size_t(a.group) * (16 + kWarps * 8);
-  if (smem > kMaxSmem) return cudaErrorInvalidValue;  // thousands of heads per kv head
+  const size_t smem = keep ? bytes(size) : pairs;  // pairs: below 144 KB, as a group has at most kMassHeads heads
   static std::atomic<uint64_t> done[4];
   const int i = (keep ? 2 : 0) + (vec ? 1 : 0);
   auto k = keep ? (vec ? mass_kernel<true, true> : mass_kernel<false, true>)

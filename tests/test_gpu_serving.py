@@ -290,6 +290,14 @@ def test_attention_mass_long(t_len):
     _check_mass(s, 2, rg.random((1, 2, t_len)).astype(np.float32), None, 0.5)
 
 
+@pytest.mark.parametrize("hq,t_len", [(100, 512), (102, 510), (300, 41), (1024, 9), (1024, 700)])
+def test_attention_mass_many_heads(hq, t_len):
+    """Groups whose share of scores just fits shared memory, or does not."""
+    rg = np.random.Generator(np.random.PCG64(hq + t_len))
+    s = (rg.standard_normal((1, hq, t_len)) * 2).astype(np.float32)
+    _check_mass(s, 1, rg.random((1, 1, t_len)).astype(np.float32), None, 0.5)
+
+
 def test_attention_mass_masks_and_lengths():
     """Heads with every score −inf add nothing; scores as low as the type goes are not masks;
     what stands behind a length (NaN) is not looked at; lengths out of range count as the

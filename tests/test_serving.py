@@ -129,6 +129,8 @@ def test_mass_refusals():
                 dict(decay=math.inf), dict(s=NULL), dict(out=NULL), dict(s=P_MIS), dict(lens=P_MIS), dict(m=P_MIS),
                 dict(out=P_MIS), dict(b=1 << 30)):
         assert mass(**bad) == INVALID, bad
+    assert mass(b=(1 << 27) + 1, hq=1, hkv=1) == INVALID
+    assert mass(hq=1025, hkv=1) == UNSUPPORTED and mass(hq=1025, hkv=1, t=0) == UNSUPPORTED
     assert mass(b=0, s=NULL, out=NULL) == OK
     assert mass(t=0, s=NULL, out=NULL) == OK
 
