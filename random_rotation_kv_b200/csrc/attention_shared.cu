@@ -406,7 +406,9 @@ template <int D> cudaError_t launch_d(const SharedArgs& a, cudaStream_t stream) 
     e = launch_shared_tc(a, stream);
   }
   if (e != cudaSuccess) return e;
-  // eight warps per row while that leaves fewer than eight blocks per SM
+  // Eight warps per row while that leaves fewer than eight blocks per SM: whole calls of 512 rows
+  // with many parts 27.1 us against 28.8 with one warp, 112 rows of d = 256 22.4 against 26.2;
+  // 4096 rows 72.3 against 63.7, 16384 rows 268 against 231.
   if (rows <= 148 * 8) return launch_pdl(shared_merge_kernel<D, 8>, dim3(unsigned(rows)), dim3(256), 0, stream, a);
   return launch_pdl(shared_merge_kernel<D, 1>, blocks, dim3(256), 0, stream, a);
 }

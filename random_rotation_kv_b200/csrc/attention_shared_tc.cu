@@ -16,7 +16,12 @@
 // Units of at most 16 rows (d ≤ 128) exchange the operands' roles: a tile's 128 tokens are the
 // rows of Sᵀ = C_K·Q'ᵀ and the coordinates the rows of Oᵀ = C_Vᵀ·Pᵀ, 16 columns wide, so that a
 // thread has a token's 8 rows to weigh instead of a row's 64 tokens of which most
-// rows would be empty.
+// rows would be empty (33 sequences x 4 heads of up to 1500 tokens, 4 rows a unit: 24 us against 31
+// without; 64 x 8 tails behind a prefix of 32768 tokens: 125 against 156).
+//
+// Bound by the latency of the weight warps' two passes (about 3600 of a tile's 4400 cycles at 128
+// rows): 64 sequences x 32 heads on 32768 + 1024 tokens x 8 heads take 125 us, 280 TFLOP/s,
+// against 21 us of products at the tensor cores' rate; 16 sequences on 4096 tokens 27 us.
 //
 // One CTA per SM walks its range of tiles (128 tokens, 64 for d = 256), 19 warps:
 //  * warp 17 copies the packed codes of two tiles ahead into shared memory (TMA boxes of

@@ -13,6 +13,8 @@
 // cosine serve every head the thread walks; the heads are spread over more threads only
 // while there are too few tokens to fill the GPU.  Pairs that do not come in eights
 // (rot not a multiple of 16) and addresses off 32 bytes take one pair per thread.
+// 32768 x 8 x 128 fp16: 22-24 us, 5.6-6.0 TB/s (one pair per thread: 46 us); one token of 32
+// heads: 1.8 us.
 #include <cstring>
 
 #include "rope.h"
@@ -174,9 +176,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, const 
   }
 }
 
-// Blocks of heads: one while the tokens alone give every SM two thousand threads.
+// Blocks of heads: one while the tokens alone give every SM 1536 threads.  All heads in one thread:
+// a token of 32 heads x 128 5.8 us against 1.8, 64 tokens 8.1 against 2.3; 32768 tokens x 8
+// heads 22.4 us against 24.0 with two blocks.
 int head_blocks(int64_t threads, int heads) {
-  const int64_t want = int64_t(148) * 2048;
+  const int64_t want = int64_t(148) * 1536;
   const int64_t hb = (want + threads - 1) / threads;
   return int(hb < heads ? hb : heads);
 }
