@@ -331,7 +331,8 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  *   tk_codes    [batch·tail_cap·hkv × d·k_bits/8] bytes, row (b·tail_cap + t)·hkv + g;
  *   tk_norms, tv_codes, tv_norms likewise
  *   tail_lens   [batch] int32 on the device, read by the kernels: values outside
- *               [0, tail_cap] count as the nearer end.  Rows behind n_b are not read.
+ *               [0, tail_cap] count as the nearer end.  Rows behind n_b do not count,
+ *               whatever they hold.
  *   workspace   device scratch of workspace_bytes ≥ rrq_attention_shared_workspace_bytes(
  *               batch, hq, hkv, d, prefix, tail_cap), 256-byte aligned, of any content.
  *               Calls that share a workspace must not overlap on the GPU (also where
@@ -343,7 +344,8 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  * Alignment: codes, q and out 16 bytes, norms and tail_lens 4.
  * Accuracy: softmax statistics, sums and the rotations in fp32.  For d ≤ 256 both
  * products run on the tensor cores with fp16 operands and fp32 sums; value weights
- * are scaled so that value norms within 2^-18 of the largest one keep their precision.
+ * are scaled so that value norms within 2^-18 of the largest one keep their precision, and
+ * so are codebook levels within 2^-14 of the largest (smaller ones are rounded to 2^-25 of it).
  * The rotated queries are two fp16 parts (22 bits) for d ≤ 128 and one (11 bits, a
  * score's error up to 2^-11·scale·‖q‖·‖k̂_t‖ and on average √d times smaller) for d = 256.
  * For d ≠ 256, and for d = 256 while the scores' own error stays below 5e-4, the output

@@ -191,6 +191,10 @@ def test_shared_attention_workspace_sizes():
     ws = B.rrq_attention_shared_workspace_bytes
     assert ws(0, 8, 2, 128, 10, 10) == 0 and ws(1, 9, 2, 128, 10, 10) == 0 and ws(1, 8, 2, 100, 10, 10) == 0
     assert ws(1, 258, 2, 128, 10, 10) == 0
+    # tokens are counted in 32 bits, rounded up to a tile
+    most = (1 << 31) - 129
+    assert ws(1, 1, 1, 64, most, 0) > 0 and ws(1, 1, 1, 64, most + 1, 0) == 0
+    assert ws(3, 1, 1, 64, 0, most // 3) > 0 and ws(3, 1, 1, 64, 0, most // 3 + 1) == 0
     for d in (64, 128, 256, 512):
         rows = 4 * 32
         # a head, the queries, and at least one state (a pair and d floats) per row and part
