@@ -521,3 +521,49 @@ def test_serving_loop():
     for b in (0, 2):
         assert np.array_equal(index[b].cpu().numpy(), kept[b])
     check(cut, new_lens)
+
+
+def test_serving_calls_captured():
+    """A decode step's calls in one graph, replayed on other inputs and lengths: what the calls give
+    one by one."""
+    b, hq, hkv, d, cap, keep = 3, 8, 2, 128, 300, 90
+    freqs, factor = B.rrq_rope_frequencies(d)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    p = _part(np.random.Generator(np.random.PCG64(3)), 200 * hkv, d, 4, 4)
+    t = _part(np.random.Generator(np.random.PCG64(4)), b * cap * hkv, d, 4, 4)
+    p, t = [_dev(x) for x in p], [_dev(x) for x in t]
+    q = torch.empty(b, hq, d, device=DEV, dtype=torch.float16)
+    scores = torch.empty(b, hq, cap, device=DEV)
+    pos = torch.empty(b, device=DEV, dtype=torch.int64)
+    lens = torch.empty(b, device=DEV, dtype=torch.int32)
+    mass = torch.empty(b, hkv, cap, device=DEV)
+
+    def fill(lengths, first):
+        q.copy_(torch.randn(q.shape, device=DEV, generator=g))
+        scores.copy_(torch.randn(scores.shape, device=DEV, generator=g))
+        mass.copy_(torch.rand(mass.shape, device=DEV, generator=g))
+        lens.copy_(torch.tensor(lengths, dtype=torch.int32))
+        pos.copy_(torch.arange(b) + first)
+
+    def step():
+        turned = B.rrq_rope(q, pos, freqs, factor=factor)
+        out = B.rrq_attention_shared(turned, *p, *t, lens, hkv, d, 1, 2, scale=d ** -0.5)
+        m = B.rrq_attention_mass(scores, hkv, mass=mass, lens=lens, decay=0.5)
+        shaped = [x.view(b, cap, hkv, *x.shape[1:]) for x in t]
+        return [turned, out, m, *B.rrq_evict(m, lens, keep, *shaped, sink=4, recent=10)]
+
+    fill([300, 17, 91], 5)
+    step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            held = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for lengths, first in (([300, 17, 91], 9), ([0, 300, 90], 1 << 40), ([1, 2, 299], 0)):
+        fill(lengths, first)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(held, step()):
+            assert torch.equal(got, want)
