@@ -342,14 +342,20 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  * tail_cap = 0) may be NULL.  batch = 0 is a no-op.  d ∈ {64, 128, 256, 512}, 1- to
  * 4-bit K and V; hq a multiple of hkv, at most 128 query heads per kv head.
  * Alignment: codes, q and out 16 bytes, norms and tail_lens 4.
- * Accuracy: softmax statistics, sums and the rotations in fp32.  For d ≤ 256 both
- * products run on the tensor cores with fp16 operands and fp32 sums; value weights
- * are scaled so that value norms within 2^-18 of the largest one keep their precision, and
- * so are codebook levels within 2^-14 of the largest (smaller ones are rounded to 2^-25 of it).
- * The rotated queries are two fp16 parts (22 bits) for d ≤ 128 and one (11 bits, a
- * score's error up to 2^-11·scale·‖q‖·‖k̂_t‖ and on average √d times smaller) for d = 256.
- * For d ≠ 256, and for d = 256 while the scores' own error stays below 5e-4, the output
- * of a head is within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is rounded to q_dtype.
+ * Accuracy: softmax statistics, sums and the rotations in fp32 (all of it for d = 512).  For
+ * d ≤ 256 both products run on the tensor cores with fp16 operands and fp32 sums:
+ *  - the weights p_t·‖v̂_t‖, relative to the largest of their head: 11 bits down to 2^-18 of
+ *    it, within 2^-29 of it below, whatever p_t and ‖v̂_t‖ are on their own (value norms below
+ *    2^-90 lose precision, and weights p_t below 2^-90 of the largest may count as zero);
+ *  - the levels of a codebook: 11 bits within 2^-14 of its largest, within 2^-25 of that
+ *    below; the default ones of 1 to 3 bits to 2^-14 of themselves or better, of 4 bits to
+ *    3.8e-5 on average;
+ *  - the rotated queries: 22 bits for d ≤ 128, 11 bits for d = 256.
+ * A score is therefore off by at most 2^-11·scale·‖q‖·‖k̂_t‖ from the key levels, and as much
+ * again from the queries at d = 256; each is √d times smaller on average.  While that stays
+ * below 5e-4, and no more than 2^18 tokens of a head have weights below 2^-18 of its largest,
+ * the output of a head is within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is rounded to
+ * q_dtype.
  * Errors: RRQ_ERR_INVALID (incl. a workspace that is too small), RRQ_ERR_UNSUPPORTED
  * (q_dtype RRQ_F32, more than 128 heads per kv head, 2^31 − 128 or more tokens in the
  * prefix or over all tails, 10^8 or more tiles of 64 or 128 tokens over all units of work,

@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
     }
   }
   fwht_row(v, lane);
-  const float inv = n > 0 ? 1.f / (l * float(D) * a.v_alpha) : 0.f;
+  const float inv = n > 0 ? 1.f / l / (float(D) * a.v_alpha) : 0.f;  // l itself may be near fp32's end
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int c = 32 * k + lane;

@@ -6,12 +6,16 @@
 // d ≤ 128 a second fp16 part holds what the first rounds off, which at d = 256 the tensor
 // memory has no room for) and the levels c as fp16,
 //     S = Q'·C_Kᵀ,   x = 2^e·ν^K_t·S,   P = 2^{x − m'}·ν^V_t,   O += P·C_V,
-// where m' follows the row's running maximum m: it moves only when m grows by more than
-// 8 (powers of two), so O is rarely rescaled, and it carries the power of two that
-// brings the weights into fp16's range: with N the power of two below the largest ν^V
-// seen (it moves when that grows fourfold), m' = m − 4 + log2 N, so weights are at most
-// 2^15 and keep full precision down to 2^-18 of the largest.  The state (m', Σ 2^{x − m'}, O)
-// is what the merge takes.
+// where m' = m − 9 follows the row's running maximum m of x + log2 ν^V (so of the products
+// that are summed: a token with most of the weight and a value of no size does not push the
+// others out of fp16's range, nor does a large value without weight).  It moves only when m
+// grows by more than 6 (powers of two), so O is rarely rescaled; P is at most 2^15.  In a full
+// tile whose value norms lie within 2^5 of one another max x + max log2 ν^V stands for the
+// maximum, at most 5 above it, without a second number per token (64 sequences on a prefix of
+// 32768 tokens: 134 us, with the sum taken for every token 141); so P keeps 11 bits down
+// to 2^-18 of the row's largest at least.  Norms below 2^-90 count as 2^-90 in m, which keeps
+// 2^{x − m'} and its sum within fp32's range.  The state (m', Σ 2^{x − m'}, O) is what the
+// merge takes.
 //
 // Units of at most 16 rows (d ≤ 128) exchange the operands' roles: a tile's 128 tokens are the
 // rows of Sᵀ = C_K·Q'ᵀ and the coordinates the rows of Oᵀ = C_Vᵀ·Pᵀ, 16 columns wide, so that a
@@ -52,7 +56,8 @@ namespace {
 constexpr uint32_t kWaitLimit = 1u << 24;  // polls, a few seconds in all
 constexpr int kSoftWarps = 8, kFillWarps = 8;
 constexpr int kFill = 128;  // threads that fill K, and as many that fill V
-constexpr float kGrowth = 8.f, kRoom = 4.f;  // of a row's maximum before m' moves; of the weights above it
+constexpr float kGrowth = 6.f, kRoom = 9.f;  // of a row's maximum before m' moves; of the weights above it
+constexpr float kTight = 5.f;  // powers of two that a tile's value norms may span for the short way to m
 constexpr int kFewRows = 16;  // rows of a unit that exchanges the operands' roles
 constexpr int kThreads = (kSoftWarps + kFillWarps + 3) * 32;
 
@@ -66,8 +71,8 @@ template <int D> struct Tc {
   static constexpr uint32_t BARS = 0x400;
   static constexpr uint32_t TSLOT = 0x4C0;
   static constexpr uint32_t FAIL = 0x4D0;
-  static constexpr uint32_t VMAX = 0x500;            // [4 tiles][4 warps] largest value norm
-  static constexpr uint32_t NK = 0x800, NV = 0x1000; // [4 tiles][TN] norms
+  static constexpr uint32_t LRANGE = 0x600;          // [4 tiles][max, −min][4 warps] of the logarithms below
+  static constexpr uint32_t NK = 0x800, NV = 0x1000, LV = 0x1800;  // [4 tiles][TN] norms, log2 of the value norms
   static constexpr uint32_t PT = 0x2000;             // few rows: weights [2 tiles][2 × 64 tokens][16 rows], swizzled
   static constexpr uint32_t QB = 0x4000;             // few rows: queries [part][64 coordinates][16 rows], swizzled
   static constexpr uint32_t RS = 0x580;              // few rows: [2 segments][16] powers of two taken out of the queries
@@ -84,7 +89,7 @@ template <int D> struct Tc {
   static constexpr int S = 0, O = 2 * TN, Q = O + D, QL = Q + D / 2;
   // fp16 operands, fp32 sums, M = 128; bits 15 and 16: A, B MN-major
   static constexpr uint32_t idesc(int n) { return (1u << 4) | (uint32_t(n / 8) << 17) | ((128u / 16) << 24); }
-  static_assert(NV + 4 * TN * 4 <= PT && TILE <= 0x8000 && kTotal <= 227 * 1024, "layout");
+  static_assert(LV + 4 * TN * 4 <= PT && TILE <= 0x8000 && kTotal <= 227 * 1024, "layout");
 };
 
 // Token of row (column of S) n of a tile.
@@ -173,13 +178,11 @@ __device__ __forceinline__ float warp_max(float v) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-// The power of two that stands for a tile's largest value norm.
-__device__ __forceinline__ float norm_unit(float big) {
-  return fminf(fmaxf(__uint_as_float(__float_as_uint(big) & 0x7f800000u), 0x1p-60f), 0x1p60f);
-}
-// m' of a running maximum m and the unit N: weights 2^{x − m'}·ν are at most 2^15.
-__device__ __forceinline__ float shifted(float m, float unit) {
-  return m - kRoom + float(int(__float_as_uint(unit) >> 23) - 127);
+// log2 of a value norm for the running maximum; the approximation's error (2^-22) only moves m.
+__device__ __forceinline__ float norm_log2(float norm) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(fabsf(norm), 0x1p-90f)));
+  return y;
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
@@ -244,10 +247,12 @@ template <int B> __device__ __forceinline__ uint32_t octet_of(const uint32_t (&w
   if (sh + 8 * B > 32) v = __funnelshift_r(w[k], w[k + 1 < 4 ? k + 1 : 3], sh);
   return octet_nibbles(v & (B == 3 ? 0xffffffu : B == 2 ? 0xffffu : 0xffu), B);
 }
-// The largest of a tile's value norms, as the K-filling warps left them.
-template <int TN> __device__ __forceinline__ float tile_max(uint32_t at, int j) {
-  const float4 m = lds_f4(at + uint32_t(j & 3) * 16);
-  return TN == 128 ? fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) : fmaxf(m.x, m.y);
+// The largest and the smallest logarithm of a tile's value norms, as the K-filling warps left them.
+template <int TN> __device__ __forceinline__ float2 log2_range(uint32_t at, int j) {
+  const float4 a = lds_f4(at + uint32_t(j & 3) * 32), b = lds_f4(at + uint32_t(j & 3) * 32 + 16);
+  float2 r = make_float2(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
+  if (TN == 128) r = make_float2(fmaxf(r.x, fmaxf(a.z, a.w)), fmaxf(r.y, fmaxf(b.z, b.w)));
+  return make_float2(r.x, -r.y);
 }
 // Level pair of byte k of `w`; `lane_word` = table | copy of the lane.
 template <int K> __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_word) {
@@ -412,7 +417,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           float rs[8], m[8], mp[8], l[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r) m[r] = mp[r] = l[r] = 0.f;
-          float vn = 0.f;
           for (int i = 0; i < s.tiles; ++i, ++j) {
             ok = ok && wait_for(s_full(j), phase(j), fail);
             ok = __all_sync(kFull, ok);
@@ -426,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                 tmem_ld8(tl + uint32_t(L::S + (j & 1) * TN + 8 * half), v);
                 const float nk = __uint_as_float(lds_word(L::NK + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4));
                 nv = __uint_as_float(lds_word(L::NV + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4));
+                const float lv = __uint_as_float(lds_word(L::LV + uint32_t(j & 3) * (TN * 4) + uint32_t(ln) * 4));
                 tmem_ld_wait();
                 if (i == 0) {
                   const float4 r0 = lds_f4(L::RS + uint32_t(seg & 1) * 64 + uint32_t(half) * 32);
@@ -435,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                 float mx[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                  y[r] = live ? __uint_as_float(v[r]) * nk : -INFINITY;
-                  mx[r] = warp_max(y[r]);
+                  y[r] = __uint_as_float(v[r]) * nk;
+                  mx[r] = warp_max(live ? fmaf(y[r], rs[r], lv) : -INFINITY);
                 }
                 if (lane < 2)
                   sts_v4(wm + uint32_t(quarter) * 32 + uint32_t(lane) * 16, __float_as_uint(lane ? mx[4] : mx[0]),
@@ -453,21 +458,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 #pragma unroll
                   for (int r = 0; r < 8; ++r) mx[r] = q ? fmaxf(mx[r], x[r]) : x[r];
                 }
-                const float pw = norm_unit(tile_max<TN>(L::VMAX, j));
                 if (i == 0) {
-                  vn = pw;
 #pragma unroll
                   for (int r = 0; r < 8; ++r) {
-                    m[r] = mx[r] * rs[r];
-                    mp[r] = shifted(m[r], vn);
+                    m[r] = mx[r];
+                    mp[r] = m[r] - kRoom;
                   }
                 } else {
-                  const bool wide = pw > 4.f * vn;
-                  bool up = wide;
+                  bool up = false;
 #pragma unroll
-                  for (int r = 0; r < 8; ++r) up = up || mx[r] * rs[r] > m[r] + kGrowth;
+                  for (int r = 0; r < 8; ++r) up = up || mx[r] > m[r] + kGrowth;
                   if (up) {  // the same in every thread of the half
-                    if (wide) vn = pw;
                     ok = __all_sync(kFull, wait_for(o_done(j - 1), phase(j - 1), fail));
                     tc_fence_after();
                     uint32_t o[8];
@@ -475,8 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                     tmem_ld_wait();
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                      if (mx[r] * rs[r] > m[r] + kGrowth) m[r] = mx[r] * rs[r];
-                      const float mn = shifted(m[r], vn), f = ex2(mp[r] - mn);
+                      if (mx[r] > m[r] + kGrowth) m[r] = mx[r];
+                      const float mn = m[r] - kRoom, f = ex2(mp[r] - mn);
                       mp[r] = mn;
                       l[r] *= f;
                       o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
 
-        float m = 0.f, mp = 0.f, vn = 0.f;  // running maximum, m', N
+        float m = 0.f, mp = 0.f;  // running maximum, m'
         float l = 0.f;
         const uint32_t pair = uint32_t(1 + quarter);
         for (int i = 0; i < s.tiles; ++i, ++j) {
@@ -585,13 +586,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             const int left = s.tokens - i * TN, valid = left < TN ? left : TN;
             const bool full = valid == TN;
             const uint32_t sb = tl + uint32_t(L::S + (j & 1) * TN + half * TH);
-            const uint32_t nk = L::NK + uint32_t((j & 3) * TN + half * TH) * 4, nv = L::NV + uint32_t((j & 3) * TN + half * TH) * 4;
+            const uint32_t nk = L::NK + uint32_t((j & 3) * TN + half * TH) * 4, nv = nk + (L::NV - L::NK), lv = nk + (L::LV - L::NK);
             const uint32_t xch = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(ln) * 4;
+            const float2 rs2 = make_float2(rs, rs);
             float mx = -INFINITY;
             if (ok) {
-              // the largest score of the row's half (loops kept rolled: unrolled, the warps'
+              // the largest x + log2 ν of the row's half (loops kept rolled: unrolled, the warps'
               // different code ran out of the instruction cache)
-              auto largest = [&](auto whole) {
+              const float2 range = log2_range<TN>(L::LRANGE, j);
+              auto largest = [&](auto tight) {
 #pragma unroll 1
                 for (int h = 0; h < TH; h += 32) {
                   uint32_t v[32];
@@ -605,30 +608,36 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                     const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
                     y[k / 2] = mul2(y[k / 2], make_float2(n.x, n.y));
                     y[k / 2 + 1] = mul2(y[k / 2 + 1], make_float2(n.z, n.w));
+                    if constexpr (!decltype(tight)::value) {
+                      const float4 g = lds_f4(lv + uint32_t(h + k) * 4);
+                      y[k / 2] = fma2(y[k / 2], rs2, make_float2(g.x, g.y));
+                      y[k / 2 + 1] = fma2(y[k / 2 + 1], rs2, make_float2(g.z, g.w));
+                    }
                   }
-                  if constexpr (!decltype(whole)::value) mask(y, half * TH + h, valid, -INFINITY);
+                  if constexpr (!decltype(tight)::value) mask(y, half * TH + h, valid, -INFINITY);
 #pragma unroll
                   for (int k = 0; k < 16; k += 2) mx = fmaxf(mx, fmaxf(fmaxf(y[k].x, y[k].y), fmaxf(y[k + 1].x, y[k + 1].y)));
                 }
               };
-              if (full) largest(std::true_type{});
-              else largest(std::false_type{});
+              if (full && range.x - range.y <= kTight) {
+                largest(std::true_type{});
+                mx = fmaf(mx, rs, range.x);
+              } else {
+                largest(std::false_type{});
+              }
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + uint32_t(half) * 512), "f"(mx) : "memory");
             }
             ok = meet(pair, 64, ok);
             if (ok) {
-              mx = fmaxf(mx, __uint_as_float(lds_word(xch + uint32_t(half ^ 1) * 512))) * rs;
-              const float pw = norm_unit(tile_max<TN>(L::VMAX, j));
+              mx = fmaxf(mx, __uint_as_float(lds_word(xch + uint32_t(half ^ 1) * 512)));
               if (i == 0) {
                 m = mx;
-                vn = pw;
-                mp = shifted(m, vn);
+                mp = m - kRoom;
               } else {
-                const bool up = mx > m + kGrowth, wide = pw > 4.f * vn;
-                if (__any_sync(kFull, up || wide)) {
+                const bool up = mx > m + kGrowth;
+                if (__any_sync(kFull, up)) {
                   if (up) m = mx;
-                  if (wide) vn = pw;
-                  const float mn = shifted(m, vn), f = ex2(mp - mn);
+                  const float mn = m - kRoom, f = ex2(mp - mn);
                   mp = mn;
                   l *= f;
                   ok = __all_sync(kFull, wait_for(o_done(j - 1), phase(j - 1), fail));
@@ -646,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                 }
               }
               // weights into S's columns, the sum of the exponentials
-              const float2 rs2 = make_float2(rs, rs), mp2 = make_float2(-mp, -mp);
+              const float2 mp2 = make_float2(-mp, -mp);
               const uint32_t pb = sb;  // the first half of the columns that this thread reads
               float2 s2 = make_float2(0.f, 0.f), s3 = s2;
               auto weigh = [&](auto whole) {
@@ -775,8 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         const uint32_t slot = uint32_t(j & 3) * (TN * 4) + uint32_t(n) * 4;
         *reinterpret_cast<float*>(at(L::NK + slot)) = norm_k;
         *reinterpret_cast<float*>(at(L::NV + slot)) = norm_v;
-        const float big = warp_max(fabsf(norm_v));
-        if (lane == 0) *reinterpret_cast<float*>(at(L::VMAX + uint32_t(j & 3) * 16 + uint32_t(n >> 5) * 4)) = big;
+        const float lv = norm_log2(norm_v), hi = warp_max(lv), lo = warp_max(-lv);
+        *reinterpret_cast<float*>(at(L::LV + slot)) = lv;
+        if (lane < 2)
+          *reinterpret_cast<float*>(at(L::LRANGE + uint32_t(j & 3) * 32 + uint32_t(lane) * 16 + uint32_t(n >> 5) * 4)) = lane ? lo : hi;
       }
       ok = __all_sync(kFull, ok);
       if (!ok) break;
