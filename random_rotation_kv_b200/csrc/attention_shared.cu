@@ -443,9 +443,10 @@ bool attention_shared_plan(SharedArgs* a) {
   a->min_cost = kMinTiles * 10;
   int64_t per = (punits * pt * a->pcost + a->grid - 1) / a->grid;  // a range is never shorter
   if (per < a->min_cost) per = a->min_cost;
-  auto parts = [per](int64_t tiles, int cost) {
+  auto parts = [&](int64_t tiles, int cost) {
     const int64_t p = tiles > 0 ? (tiles - 1) * cost / per + 2 : 0;
-    return int(p < tiles ? p : tiles);
+    const int64_t most = tiles < a->grid ? tiles : a->grid;  // at least a tile each, one per range
+    return int(p < most ? p : most);
   };
   a->parts_p = parts(pt, a->pcost);
   a->parts_t = parts(tt, a->tcost);
