@@ -424,7 +424,7 @@ def rrq_qjl_matrix(seed: int, d: int, device=None) -> torch.Tensor:
 
 
 # ---- serving calls.  A decode step issues these every few microseconds, so they hand
-# plain integers to ctypes and ask torch for the raw stream.
+# plain integers to ctypes and ask torch for the raw stream.  Only rrq_rope records a graph.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _F32, _U8, _I32, _I64 = torch.float32, torch.uint8, torch.int32, torch.int64
 _HALVES = (torch.float16, torch.bfloat16)
@@ -631,16 +631,38 @@ def rrq_rope_frequencies(rot: int, base: float = 10000.0, schedule: str = "none"
     return out, factor.value
 
 
+class _Rope(torch.autograd.Function):
+    """The rotation and, as its gradient, the transposed map."""
+
+    @staticmethod
+    def forward(ctx, x, positions, freqs, interleaved, factor, inverse):
+        ctx.save_for_backward(positions)
+        ctx.how = freqs, interleaved, factor, inverse
+        return rrq_rope(x, positions, freqs, interleaved, factor, inverse)
+
+    @staticmethod
+    def backward(ctx, grad):
+        freqs, interleaved, factor, inverse = ctx.how
+        (positions,) = ctx.saved_tensors
+        return rrq_rope(grad.contiguous(), positions, freqs, interleaved, factor, not inverse), None, None, None, None, None
+
+
 def rrq_rope(x: torch.Tensor, positions: torch.Tensor, freqs, interleaved: bool = False,
              factor: float = 1.0, inverse: bool = False, out=None):
     """Rotary positions of x [n, heads, d] at int64 positions [n]: the first 2*len(freqs)
     coordinates of every vector turned, the rest copied; ``inverse`` applies the transposed
     map (the gradient with respect to x).  ``freqs``: radians per position on the host
-    (float64, as rrq_rope_frequencies returns them).  ``out`` may be ``x``."""
+    (float64, as rrq_rope_frequencies returns them).  ``out`` may be ``x``.
+
+    Differentiable in x (positions must then stay as they are until the backward pass); a call
+    with ``out`` records no graph.  As for any torch operation, a backward pass is captured
+    into a CUDA graph only while no graph of the same leaf from another stream is alive."""
     dev = _first(x, "x", DTYPE_CODE)
     shape, dtype = x.shape, x.dtype
     if len(shape) != 3:
         raise ValueError("x must be [n, heads, d]")
+    if out is None and x.requires_grad and torch.is_grad_enabled():
+        return _Rope.apply(x, positions, np.array(freqs, dtype=np.float64), interleaved, factor, inverse)
     n, heads, d = shape
     fr = np.ascontiguousarray(freqs, dtype=np.float64)
     if out is None:

@@ -1,5 +1,6 @@
 """The serving calls where their numbers leave the ordinary range (needs a B200): weights times
-value norms over many orders.  Tolerances as in test_gpu_serving.py."""
+value norms over many orders; rotary positions in a graph of gradients.  Tolerances as in
+test_gpu_serving.py."""
 
 from __future__ import annotations
 
@@ -8,7 +9,9 @@ import pytest
 import torch
 
 from oracle import rrq as orc
-from tests.test_gpu_serving import _attend, _check_attention, _part
+from oracle import serving as osv
+from random_rotation_kv_b200 import binding as B
+from tests.test_gpu_serving import DEV, HALF, _attend, _check_attention, _dev, _part
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +61,68 @@ def test_attention_shared_value_norms_zero(d, hq):
     assert torch.all(_attend(q, p, None, None, 1, d, 4, 4, d ** -0.5, torch.float16) == 0)
     p[3][7] = 1.0  # one value among them
     _check_attention(q, p, None, [0], 1, d, 4, 4, d ** -0.5, torch.bfloat16, "one value")
+
+
+# --------------------------------------------------------------------------------- rope
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("interleaved,inverse,rot", [(False, False, 64), (True, False, 40), (False, True, 30)])
+def test_rope_records_its_gradient(dtype, interleaved, inverse, rot):
+    """The gradient of <g, rope(x)> is the transposed map of g, whatever g's strides are."""
+    rg = np.random.Generator(np.random.PCG64(rot))
+    freqs, factor = B.rrq_rope_frequencies(rot, 10000.0, "yarn", 4.0)
+    pos = _dev(np.array([3, 1 << 20, -7], np.int64))
+    x = _dev(rg.standard_normal((3, 2, 64)), dtype).requires_grad_()
+    for g in (_dev(rg.standard_normal((3, 2, 64)), dtype), _dev(rg.standard_normal((64, 2, 3)), dtype).permute(2, 1, 0),
+              torch.ones((), dtype=dtype, device=DEV).expand(3, 2, 64)):
+        y = B.rrq_rope(x, pos, freqs, interleaved=interleaved, factor=factor, inverse=inverse)
+        with torch.no_grad():
+            plain = B.rrq_rope(x, pos, freqs, interleaved=interleaved, factor=factor, inverse=inverse)
+        assert torch.equal(y, plain) and not plain.requires_grad
+        (got,) = torch.autograd.grad(y, x, g)
+        want, size = osv.rope(g.double().cpu().numpy(), pos.cpu().numpy(), freqs, interleaved, factor, not inverse)
+        tol = size * (12 * 2.0 ** -24 + 2 * np.pi * (2.0 ** -32 + 2.0 ** 20 * 2.0 ** -65)) + HALF[dtype] * np.abs(want) + 2.0 ** -25
+        assert got.dtype == dtype and np.all(np.abs(got.double().cpu().numpy() - want) <= tol)
+
+
+def test_rope_gradient_of_the_gradient_and_what_it_keeps():
+    rg = np.random.Generator(np.random.PCG64(3))
+    freqs, _ = B.rrq_rope_frequencies(64)
+    held = freqs.copy()
+    pos = _dev(np.arange(4))
+    x = _dev(rg.standard_normal((4, 2, 64)), torch.float32).requires_grad_()
+    g = _dev(rg.standard_normal((4, 2, 64)), torch.float32).requires_grad_()
+    (gx,) = torch.autograd.grad(B.rrq_rope(x, pos, freqs), x, g, create_graph=True)
+    h = _dev(rg.standard_normal((4, 2, 64)), torch.float32)
+    (gg,) = torch.autograd.grad(gx, g, h)
+    assert torch.equal(gg, B.rrq_rope(h, pos, freqs))
+    # the frequencies are the call's own; positions that moved are refused
+    y = B.rrq_rope(x, pos, freqs)
+    freqs[:] = 0
+    (gx,) = torch.autograd.grad(y, x, h)
+    assert torch.equal(gx, B.rrq_rope(h, pos, held, inverse=True))
+    y = B.rrq_rope(x, pos, held)
+    pos += 1
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, x, h)
+
+
+def test_rope_gradient_captured():
+    """Both directions in one graph."""
+    rg = np.random.Generator(np.random.PCG64(4))
+    freqs, _ = B.rrq_rope_frequencies(64)
+    pos = _dev(np.arange(4))
+    x = _dev(rg.standard_normal((4, 2, 64)), torch.float32).requires_grad_()
+    g = _dev(rg.standard_normal((4, 2, 64)), torch.float32)
+    want = B.rrq_rope(x.detach(), pos, freqs)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        torch.autograd.grad(B.rrq_rope(x, pos, freqs), x, g)
+        with torch.cuda.graph(graph, stream=side):
+            y = B.rrq_rope(x, pos, freqs)
+            (gx,) = torch.autograd.grad(y, x, g)
+    torch.cuda.current_stream().wait_stream(side)
+    g.copy_(g.flip(0))
+    graph.replay()
+    assert torch.equal(y, want) and torch.equal(gx, B.rrq_rope(g, pos, freqs, inverse=True))
