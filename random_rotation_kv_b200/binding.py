@@ -22,8 +22,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librrq.so")
 RRQ_OK, RRQ_ERR_INVALID, RRQ_ERR_CUDA, RRQ_ERR_UNSUPPORTED, RRQ_ERR_SCRATCH = 0, 1, 2, 3, 4
 RRQ_F32, RRQ_F16, RRQ_BF16 = 0, 1, 2
 DTYPE_CODE = {torch.float32: RRQ_F32, torch.float16: RRQ_F16, torch.bfloat16: RRQ_BF16}
-# GGML block types (ggml's own type numbers), as in include/rrq.h
 ROPE_SCHEDULES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+# GGML block types (ggml's own type numbers), as in include/rrq.h
 GGML_TYPES = {"q4_0": 2, "q4_1": 3, "q5_0": 6, "q5_1": 7, "q8_0": 8}
 
 _c_i64 = ctypes.c_int64
