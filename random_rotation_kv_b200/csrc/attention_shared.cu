@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a) {
 }
 
 int sm_count() {
-  int dev = 0, sms = 148;
+  int dev = 0, sms = kSms;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   return sms < 1 ? 1 : sms;
 }
@@ -406,10 +406,11 @@ template <int D> cudaError_t launch_d(const SharedArgs& a, cudaStream_t stream) 
     e = launch_shared_tc(a, stream);
   }
   if (e != cudaSuccess) return e;
-  // Eight warps per row while that leaves fewer than eight blocks per SM: whole calls of 512 rows
-  // with many parts 27.1 us against 28.8 with one warp, 112 rows of d = 256 22.4 against 26.2;
-  // 4096 rows 72.3 against 63.7, 16384 rows 268 against 231.
-  if (rows <= 148 * 8) return launch_pdl(shared_merge_kernel<D, 8>, dim3(unsigned(rows)), dim3(256), 0, stream, a);
+  // Eight warps per row while that leaves at most six blocks per SM.  Whole calls with eight warps
+  // against one: d = 128 at 512 rows 27.9 us against 29.9, 768 rows 32.7 against 33.8, 1024 rows
+  // 37.6 against 36.6, 4096 rows 87.1 against 77.2; d = 64 and 256 at 512 rows 21.5 against 22.8 and 29.2
+  // against 32.0, at 1152 rows 27.1 against 26.6 and 41.0 against 39.8.
+  if (rows <= int64_t(a.grid) * 6) return launch_pdl(shared_merge_kernel<D, 8>, dim3(unsigned(rows)), dim3(256), 0, stream, a);
   return launch_pdl(shared_merge_kernel<D, 1>, blocks, dim3(256), 0, stream, a);
 }
 

@@ -20,8 +20,8 @@
 // Units of at most 16 rows (d ≤ 128) exchange the operands' roles: a tile's 128 tokens are the
 // rows of Sᵀ = C_K·Q'ᵀ and the coordinates the rows of Oᵀ = C_Vᵀ·Pᵀ, 16 columns wide, so that a
 // thread has a token's 8 rows to weigh instead of a row's 64 tokens of which most
-// rows would be empty (33 sequences x 4 heads of up to 1500 tokens, 4 rows a unit: 24 us against 31
-// without; 64 x 8 tails behind a prefix of 32768 tokens: 125 against 156).
+// rows would be empty (33 sequences x 4 heads of up to 1500 tokens, 4 rows a unit: 23 us against 27
+// without; 64 x 8 tails behind a prefix of 32768 tokens: 127 against 159).
 //
 // Bound by the latency of the weight warps' two passes (about 3600 of a tile's 4400 cycles at 128
 // rows): 64 sequences x 32 heads on 32768 + 1024 tokens x 8 heads take 125 us, 280 TFLOP/s,
@@ -58,7 +58,10 @@ constexpr int kSoftWarps = 8, kFillWarps = 8;
 constexpr int kFill = 128;  // threads that fill K, and as many that fill V
 constexpr float kGrowth = 6.f, kRoom = 9.f;  // of a row's maximum before m' moves; of the weights above it
 constexpr float kTight = 5.f;  // powers of two that a tile's value norms may span for the short way to m
-constexpr int kFewRows = 16;  // rows of a unit that exchanges the operands' roles
+// Rows of a unit that exchanges the operands' roles, as many as its 16 columns hold: 33 x 4 tails of up
+// to 1500 tokens at 4, 8, 12 and 16 rows 22, 24, 26 and 26 us (29, 29, 33 and 34 without); one
+// sequence of 65536 tokens x 8 heads 54, 55, 58 and 58 (62, 63, 64 and 64).
+constexpr int kFewRows = 16;
 constexpr int kThreads = (kSoftWarps + kFillWarps + 3) * 32;
 
 template <int D> struct Tc {

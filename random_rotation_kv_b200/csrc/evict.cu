@@ -288,7 +288,7 @@ template <typename U> cudaError_t launch_move(const EvictArgs& a, cudaStream_t s
   const int64_t most = a.keep < a.cap ? a.keep : a.cap;
   const int64_t blocks = (most * a.hkv + kMoveRows - 1) / kMoveRows;
   const unsigned y = unsigned(a.batch < 65535 ? a.batch : 65535);
-  const int64_t fill = (int64_t(148) * 16 + y - 1) / y;
+  const int64_t fill = (int64_t(kSms) * 16 + y - 1) / y;
   return launch_pdl(evict_move_kernel<U>, dim3(unsigned(blocks < fill ? blocks : fill), y), dim3(kMoveThreads), 0, stream, a);
 }
 

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, const 
 // a token of 32 heads x 128 5.8 us against 1.8, 64 tokens 8.1 against 2.3; 32768 tokens x 8
 // heads 22.4 us against 24.0 with two blocks.
 int head_blocks(int64_t threads, int heads) {
-  const int64_t want = int64_t(148) * 1536;
+  const int64_t want = int64_t(kSms) * 1536;
   const int64_t hb = (want + threads - 1) / threads;
   return int(hb < heads ? hb : heads);
 }

@@ -9,6 +9,7 @@
 
 namespace rrq {
 
+constexpr int kSms = 148;       // SMs of a B200, for rules that only weigh launch shapes
 constexpr int kMaxLevels = 16;  // bits <= 4
 constexpr int kMaxCells = 64;   // cell-table search: at most 64 + 1 cells
 
