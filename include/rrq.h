@@ -323,8 +323,9 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  * query head h, g = ⌊h·hkv/hq⌋, over the tokens t of the prefix and then of the
  * first n_b = tail_lens[b] rows of tail b:
  *     s[t] = scale · <q_{b,h}, k̂_{t,g}>,   p = softmax(s),   out_{b,h} = Σ_t p[t]·v̂_{t,g},
- * k̂ and v̂ as rrq_decode.  The prefix is read and dequantised once for the whole
- * batch.  A sequence without any token (no prefix and n_b = 0) gets zeros.
+ * k̂ and v̂ as rrq_decode.  The prefix is read and dequantised once for every 128 query rows
+ * (sequences × heads per kv head; for d = 512, a plain kernel, it is dequantised once for
+ * every 8).  A sequence without any token (no prefix and n_b = 0) gets zeros.
  *   q           [batch × hq × d] of q_dtype (RRQ_F16 or RRQ_BF16), unrotated
  *   pk_codes    [prefix·hkv × d·k_bits/8] bytes, row t·hkv + g;  pk_norms [prefix·hkv]
  *   pv_codes    [prefix·hkv × d·v_bits/8] bytes;                 pv_norms [prefix·hkv]
@@ -387,6 +388,9 @@ size_t rrq_attention_shared_workspace_bytes(int64_t batch, int hq, int hkv, int 
  * scores over the tokens t < n_b = lens[b]:
  *     out[b][g][t] = decay · mass[b][g][t] + Σ_{h in group g} p[b][h][t],   t < n_b,
  *     out[b][g][t] = mass[b][g][t],                                        t ≥ n_b.
+ * The weights are those among the tokens whose scores are given.  For a sequence behind a
+ * shared prefix pass the scores of prefix and tail together: with the tail's alone the
+ * weights of its tokens add up to 1 per head, whatever the prefix draws.
  * A score of −inf masks its token (weight 0); a head whose scores are all −inf adds
  * nothing.  +inf and NaN scores give unspecified values for the tokens of their
  * kv head (no fault).
@@ -415,7 +419,9 @@ int rrq_attention_mass(const float* scores, int64_t batch, int hq, int hkv, int6
  *     index[b][g][s] = the s-th kept token (ascending), s < m_b;
  *     row (b·keep + s)·hkv + g of the output cache = row (b·cap + index[b][g][s])·hkv + g;
  *     out_mass[b][g][s] = mass[b][g][index[b][g][s]].
- * Entries s ≥ m_b of every output are left as they were.
+ * Entries s ≥ m_b of every output are left as they were.  The new cache's capacity is keep: a
+ * full one has no room for a next token.  To evict into caches of more tokens, call once
+ * per sequence (batch = 1) with the beginning of that sequence's cache as the output.
  *   mass      [batch × hkv × cap] float (a NaN counts as less than −inf, −0 as +0)
  *   lens      [batch] int32 on the device, or NULL (all cap tokens); values outside
  *             [0, cap] count as the nearer end
@@ -469,8 +475,8 @@ int rrq_rope_frequencies(int schedule, int rot, double base, double stretch, dou
  * and coordinates from rot on are copied.  inverse = 1 takes −φ: the transposed map,
  * which is also the gradient with respect to x.
  * The angle is formed as p times the frequency in turns as a 64-bit fixed-point
- * fraction, modulo one turn: within |p|·2^-65 turns of the exact one.  Products in
- * fp32, rounded once to dtype.
+ * fraction, modulo one turn, and cut to 32 bits: within 2^-32 + |p|·2^-65 turns of the
+ * exact one.  Products in fp32, rounded once to dtype.
  *   x          [n × heads × d] of dtype;  y the same (output), which may be x itself
  *   positions  [n] int64 on the device, of any sign
  *   freqs      HOST, double[rot/2], finite, |freqs| < 2^31

@@ -752,8 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     Cursor c(a, range);
     uint32_t kw[2][4];  // rows that no box moves (d = 64)
     float norm_k = 0.f, norm_v = 0.f;
-    // what comes from global memory for the cursor's tile; rows past the end repeat the last (not
-    // through L1: the launch that wrote them may still have run when this one began)
+    // what comes from global memory for the cursor's tile, past L1 as it is read once; rows past the
+    // end repeat the last
     auto fetch = [&] {
       const int tt = c.i * TN + tok, part = c.s.flags & 1;
       const bool in = tt < c.s.tokens;

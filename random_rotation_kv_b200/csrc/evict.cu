@@ -12,8 +12,9 @@
 // counts' prefixes give each kept token its slot, and of the equal ones the first are
 // kept; so the order of blocks and atomics never shows in the result.  The passes are bound
 // by their four cluster barriers, not by the masses, which are read once.
-// Loads of what another launch may have written bypass L1 (also in mass.cu): launches overlap,
-// so this kernel may have begun before that one ended.
+// Launches overlap, so this kernel may have begun before the one that wrote its inputs ended; every
+// load comes after pdl_wait, which makes those writes visible, and none is through the read-only
+// path.  What is read once is loaded past L1.
 // Moving: a second launch over all SMs copies the rows, 128 per block, 16 bytes (8 where rows
 // are not a multiple of 16) per access with the code rows of the new cache written in
 // one run; it is bound by memory (2·(d·(kb + vb)/8 + 8) bytes per kept row).

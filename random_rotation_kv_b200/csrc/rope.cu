@@ -2,11 +2,11 @@
 // token's angle.
 //
 // (a', b') = factor·(a·cos φ − b·sin φ, a·sin φ + b·cos φ), φ = p·θ_i.  The angle is
-// needed modulo one turn only, so θ_i comes as the 64-bit fraction θ_i/2π·2^64 and
-// p·θ_i is one wrapping 64-bit product: exact for every int64 position, where an
-// fp32 product would lose all digits of φ from p ≈ 10^6 on.  The top 32 bits are split
-// into the nearest quarter turn (which swaps and negates) and a remainder of at most
-// an eighth of a turn, whose sine and cosine are taken in fp32.
+// needed modulo one turn only, so θ_i comes as the 64-bit fraction θ_i/2π·2^64, rounded, and
+// p·θ_i is one wrapping 64-bit product: within |p|·2^-65 turns for every int64 position, where an
+// fp32 product would lose all digits of φ from p ≈ 10^6 on.  Its top 32 bits (cut: 2^-32 turns or
+// 1.5e-9 more) are split into the nearest quarter turn (which swaps and negates) and a
+// remainder of at most an eighth of a turn, whose sine and cosine are taken in fp32.
 //
 // Bound by memory: x is read once and y written once.  A thread owns eight pairs of one
 // token (two runs of 8 coordinates, or one of 16) and walks heads with them, so a sine and

@@ -312,3 +312,34 @@ def test_rope_addresses(dtype, interleaved, rot):
         tol = size * (12 * 2.0 ** -24 + 2 * math.pi * (2.0 ** -32 + far * 2.0 ** -65)) + HALF[dtype] * np.abs(want) + 2.0 ** -25
         assert np.all(np.abs(got - want)[..., :rot] <= tol[..., :rot])
         assert np.array_equal(got[..., rot:], x.double().cpu().numpy()[..., rot:])
+
+
+# ------------------------------------------------------------------------ all together
+def test_evicted_caches_grow():
+    """Sequences evicted one by one into the beginning of larger caches, a token appended to each, and
+    attention over them: against the oracle on the same rows."""
+    rg = np.random.Generator(np.random.PCG64(51))
+    batch, hq, hkv, d, cap, keep = 3, 8, 2, 128, 90, 40
+    t = [_dev(x).view(batch, cap, hkv, *x.shape[1:]) for x in _part(rg, batch * cap * hkv, d, 4, 4)]
+    lens = _dev(np.array([90, 25, 41], np.int32))
+    mass = _dev(rg.random((batch, hkv, cap)).astype(np.float32))
+    new = [torch.zeros_like(x) for x in t]
+    new_lens = torch.empty_like(lens)
+    for b in range(batch):
+        one = slice(b, b + 1)
+        B.rrq_evict(mass[one], lens[one], keep, *(x[one] for x in t), sink=2, recent=5, out_lens=new_lens[one],
+                    out=[x[one, :keep] for x in new])
+    kept = osv.evict(mass.cpu().numpy(), lens.cpu().numpy(), keep, 2, 5)
+    assert new_lens.tolist() == [40, 25, 40]
+    for x, old in zip(new, t):
+        for b in range(batch):
+            for g in range(hkv):
+                assert torch.equal(x[b, :len(kept[b][g]), g], old[b, torch.from_numpy(kept[b][g]).to(DEV), g])
+                assert torch.all(x[b, len(kept[b][g]):, g] == 0)
+    at = new_lens.long()
+    for w, bits, seed in ((0, 4, 42), (2, 4, 43)):
+        codes, norms = B.rrq_encode(_dev(rg.standard_normal((batch, hkv, d)), torch.float16), bits, seed)
+        new[w][torch.arange(batch, device=DEV), at], new[w + 1][torch.arange(batch, device=DEV), at] = codes, norms
+    host = [x.reshape(-1, *x.shape[3:]).cpu().numpy() for x in new]
+    _check_attention(rg.standard_normal((batch, hq, d)), None, host, (at + 1).tolist(), hkv, d, 4, 4, d ** -0.5, torch.float16,
+                     "grown")
