@@ -351,10 +351,9 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  *  - the levels of a codebook: 11 bits within 2^-14 of its largest, within 2^-25 of that
  *    below; the default ones of 1 to 3 bits to 2^-14 of themselves or better, of 4 bits to
  *    3.8e-5 on average;
- *  - the rotated queries: 22 bits for d ≤ 128, 11 bits for d = 256.
- * A score is therefore off by at most 2^-11·scale·‖q‖·‖k̂_t‖ from the key levels, and as much
- * again from the queries at d = 256; each is √d times smaller on average.  While that stays
- * below 5e-4, and no more than 2^18 tokens of a head have weights below 2^-18 of its largest,
+ *  - the rotated queries: 22 bits.
+ * A score is therefore off by at most 2^-11·scale·‖q‖·‖k̂_t‖, and √d times less on average, all
+ * but 2^-11 of it from the key levels.  While that stays below 5e-4, and no more than 2^18 tokens of a head have weights below 2^-18 of its largest,
  * the output of a head is within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is rounded to
  * q_dtype.
  * Errors: RRQ_ERR_INVALID (incl. a workspace that is too small), RRQ_ERR_UNSUPPORTED

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(256) shared_prepare_kernel(const SharedArgs a)
       const float x = v[i] * f;
       const __half hi = __float2half_rn(x);
       a.qh[to * D + 32 * i + lane] = hi;
-      if constexpr (D <= 128) a.ql[to * D + 32 * i + lane] = __float2half_rn(x - __half2float(hi));
+      a.ql[to * D + 32 * i + lane] = __float2half_rn(x - __half2float(hi));
     }
   }
 }

@@ -53,7 +53,7 @@ struct SharedArgs {
   int4* segs;     // two words per segment, those of a range one after the other (SharedSegment)
   float* qrot;    // rotated queries, row (g·rows + r), d values (d = 512), or in their place
   __half* qh;     //   the same as fp16 times a power of two per row,
-  __half* ql;     //   what that rounding left (d ≤ 128),
+  __half* ql;     //   what that rounding left,
   float* qexp;    //   and the power of two taken out
   float2* stats;  // (m, l) of part p, kv head g, row r at (p·hkv + g)·rows + r; prefix parts, then tail parts
   float* acc;     // the same rows × d

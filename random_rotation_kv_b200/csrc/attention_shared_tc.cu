@@ -2,9 +2,8 @@
 // 5th-generation tensor cores, for head sizes up to 256: up to 128 query rows against a
 // run of tiles of one kv head (attention_shared.h).
 //
-// With the rows' rotated queries q' (fp16, a power of two 2^-e per row taken out; at
-// d ≤ 128 a second fp16 part holds what the first rounds off, which at d = 256 the tensor
-// memory has no room for) and the levels c as fp16,
+// With the rows' rotated queries q' (two fp16 parts, the second what the first rounds off, and a
+// power of two 2^-e per row taken out) and the levels c as fp16,
 //     S = Q'·C_Kᵀ,   x = 2^e·ν^K_t·S,   P = 2^{x − m'}·ν^V_t,   O += P·C_V,
 // where m' = m − 9 follows the row's running maximum m of x + log2 ν^V (so of the products
 // that are summed: a token with most of the weight and a value of no size does not push the
@@ -41,7 +40,10 @@
 //  * warps 0–7 make the weights: two threads per query row with half of the tokens each,
 //    the row's maximum met through shared memory, weights back into S's own columns as
 //    fp16 (or, for few rows, a thread per token and 8 rows, weights into shared memory).
-// Tensor memory: S twice, O and the queries (all of its 512 columns at d = 256).
+// Tensor memory: S twice, O and the queries, of which d = 256 has room for the first part only (512
+// columns in use): its second part is an operand in shared memory, in place of three quarters of
+// the tables' copies and of what few rows take elsewhere (32 sequences x 32/8 heads on 8192
+// tokens 66 us, with one part of 11 bits and all copies 52; 7 x 16/4 heads on 2049: 25.4 and 22.4).
 // Every wait is bounded; a wait that gives up makes the CTA's states NaN.
 #include <cstring>
 
@@ -84,15 +86,19 @@ template <int D> struct Tc {
   __host__ __device__ static constexpr uint32_t piece(int stage, int v, int half) {
     return 0x8000u + uint32_t(stage * 4 + v * 2 + half) * 0x1000u;
   }
-  static constexpr uint32_t TABLE = 0x10000;         // K pairs at +0, V pairs at +128 of every 256 bytes
+  // pairs of levels, COPIES to an entry: K and V alternating (32) or one table after the other (8)
+  static constexpr int COPIES = D <= 128 ? 32 : 8;
+  static constexpr uint32_t TABLE = 0x10000, VTABLE = COPIES == 32 ? COPIES * 4 : 256 * COPIES * 4;
   static constexpr uint32_t K0 = 0x20000;            // K stages of 32 KB
+  // d = 256: second query part, 64 coordinates of the 128 rows per block of 16 KB, swizzled
+  __host__ __device__ static constexpr uint32_t qlow(int block) { return block < 3 ? 0x14000u + uint32_t(block) * 0x4000u : 0x2000u; }
   static constexpr uint32_t VT = 0x30000;            // V tile
   static constexpr size_t kTotal = 0x38000 - kBase;
   // tensor memory columns
   static constexpr int S = 0, O = 2 * TN, Q = O + D, QL = Q + D / 2;
   // fp16 operands, fp32 sums, M = 128; bits 15 and 16: A, B MN-major
   static constexpr uint32_t idesc(int n) { return (1u << 4) | (uint32_t(n / 8) << 17) | ((128u / 16) << 24); }
-  static_assert(LV + 4 * TN * 4 <= PT && TILE <= 0x8000 && kTotal <= 227 * 1024, "layout");
+  static_assert(LV + 4 * TN * 4 <= PT && TABLE + 256 * 2 * COPIES * 4 <= (D <= 128 ? K0 : qlow(0)) && qlow(3) + 0x4000 <= XCH && TILE <= 0x8000 && kTotal <= 227 * 1024, "layout");
 };
 
 // Token of row (column of S) n of a tile.
@@ -257,20 +263,23 @@ template <int TN> __device__ __forceinline__ float2 log2_range(uint32_t at, int 
   if (TN == 128) r = make_float2(fmaxf(r.x, fmaxf(a.z, a.w)), fmaxf(r.y, fmaxf(b.z, b.w)));
   return make_float2(r.x, -r.y);
 }
-// Level pair of byte k of `w`; `lane_word` = table | copy of the lane.
-template <int K> __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_word) {
-  return lds_u32(__byte_perm(w, lane_word, K == 0 ? 0x7604u : K == 1 ? 0x7614u : K == 2 ? 0x7624u : 0x7634u));
+// Level pair of byte k of `w`; `lane_word` = table | copy of the lane.  Entries of 256 or 32 bytes.
+template <int COPIES, int K> __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_word) {
+  if constexpr (COPIES == 32)
+    return lds_u32(__byte_perm(w, lane_word, K == 0 ? 0x7604u : K == 1 ? 0x7614u : K == 2 ? 0x7624u : 0x7634u));
+  else
+    return lds_u32(((K == 0 ? w << 5 : w >> (8 * K - 5)) & 0x1fe0u) | lane_word);
 }
 
 // Four octets of a token's row as levels, chunks c0 .. c0 + 3 of `row`.  All
 // lookups come before the first store: a load is not moved ahead of a store that might alias it.
-template <int B> __device__ __forceinline__ void put_octets(const uint32_t (&w)[4], uint32_t row, int c0, int n, uint32_t lane_word) {
+template <int COPIES, int B> __device__ __forceinline__ void put_octets(const uint32_t (&w)[4], uint32_t row, int c0, int n, uint32_t lane_word) {
   uint32_t p[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t x = octet_of<B>(w, i);
-    p[i][0] = pair_of<0>(x, lane_word), p[i][1] = pair_of<1>(x, lane_word);
-    p[i][2] = pair_of<2>(x, lane_word), p[i][3] = pair_of<3>(x, lane_word);
+    p[i][0] = pair_of<COPIES, 0>(x, lane_word), p[i][1] = pair_of<COPIES, 1>(x, lane_word);
+    p[i][2] = pair_of<COPIES, 2>(x, lane_word), p[i][3] = pair_of<COPIES, 3>(x, lane_word);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -313,7 +322,6 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ SharedMaps maps) {
   using L = Tc<D>;
   constexpr int TN = L::TN;
-  constexpr bool SPLIT = D <= 128;
   extern __shared__ __align__(1024) uint8_t dsm[];
   pdl_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -355,12 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   // entry b of the tables: the levels of its low and its high nibble
-  for (int i = tid; i < 256 * 64 && placed; i += kThreads) {
-    const int b = i >> 6;
-    const float* lev = i & 32 ? a.v_levels : a.k_levels;
-    const float f = i & 32 ? a.v_alpha : a.k_alpha;
+  for (int i = tid; i < 256 * 2 * L::COPIES && placed; i += kThreads) {
+    const int v = (i / L::COPIES) & 1, b = i / (2 * L::COPIES);
+    const float* lev = v ? a.v_levels : a.k_levels;
+    const float f = v ? a.v_alpha : a.k_alpha;
     const __half2 h = __floats2half2_rn(lev[b & 15] * f, lev[b >> 4] * f);
-    *reinterpret_cast<__half2*>(at(L::TABLE + uint32_t(b) * 256 + uint32_t(i & 63) * 4)) = h;
+    const uint32_t entry = L::COPIES == 32 ? uint32_t(b) * 256 : uint32_t(b) * (L::COPIES * 4);
+    *reinterpret_cast<__half2*>(at(L::TABLE + entry + (v ? L::VTABLE : 0u) + uint32_t(i & (L::COPIES - 1)) * 4)) = h;
   }
   tc_fence_before();
   __syncthreads();
@@ -378,14 +387,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     bool staged = false;  // the segment's queries are in shared memory already
     // few rows: the queries of a segment as an operand, rows past its own as zeros; read from
     // global memory a segment before they are staged
-    uint4 qv[SPLIT ? 2 : 1];
+    uint4 qv[2];
     float qe = 1.f;
     const int q_row = (tid >> 3) & 15, q_chunk = (tid & 7) + ((tid >> 7) << 3);  // row, chunk of 8 coordinates
     auto read_queries = [&](const SharedSegment& s) {
       const int64_t qrow = int64_t(s.g) * a.rows + s.row0;
       if (q_row < s.nrows && q_chunk < D / 8) {
 #pragma unroll
-        for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+        for (int part = 0; part < 2; ++part)
           qv[part] = __ldcg(reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + (qrow + q_row) * D) + q_chunk);
       }
       if (tid < 16 && tid < s.nrows) qe = __ldcg(a.qexp + qrow + tid);
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     auto stage = [&](const SharedSegment& s, int number) {
       if (q_chunk < D / 8) {
 #pragma unroll
-        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+        for (int part = 0; part < 2; ++part) {
           const uint4 v = q_row < s.nrows ? qv[part] : make_uint4(0, 0, 0, 0);
           sts_v4(L::QB + uint32_t(part * (D / 64) + (q_chunk >> 3)) * 2048 + uint32_t(q_row) * 128 +
                      (uint32_t((q_chunk ^ q_row) & 7) << 4), v.x, v.y, v.z, v.w);
@@ -558,21 +567,31 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         float rs = 1.f;
         if (warp_ok) {
           rs = a.qexp[qrow];
+          const uint4* qh = reinterpret_cast<const uint4*>(a.qh + qrow * D + half * DH);
+          const uint4* ql = reinterpret_cast<const uint4*>(a.ql + qrow * D + half * DH);
 #pragma unroll
-          for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-            const uint4* q = reinterpret_cast<const uint4*>((part ? a.ql : a.qh) + qrow * D + half * DH);
+          for (int part = 0; part < (D <= 128 ? 2 : 1); ++part) {
 #pragma unroll 1
             for (int i = 0; i < DH / 32; ++i) {
               uint32_t r[16];
+              uint4 low[D <= 128 ? 1 : 4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const uint4 v = __ldcg(q + 4 * i + k);
+                const uint4 v = __ldcg((part ? ql : qh) + 4 * i + k);
                 r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
+                if constexpr (D > 128) low[k] = __ldcg(ql + 4 * i + k);
               }
               tmem_st16(tl + uint32_t((part ? L::QL : L::Q) + half * (DH / 2) + 16 * i), r);
+              if constexpr (D > 128) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // chunk 4i + k of this half's coordinates
+                  sts_v4(L::qlow(half * (DH / 64) + (i >> 1)) + uint32_t(ln) * 128 + (uint32_t((4 * i + k) ^ ln) & 7) * 16, low[k].x,
+                         low[k].y, low[k].z, low[k].w);
+              }
             }
           }
           tmem_st_wait();
+          if constexpr (D > 128) fence_proxy_async_smem();
         }
         tc_fence_before();
         __syncwarp();
@@ -747,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const int n = ft % TN, sub = ft / TN;  // row of the tile
     const int tok = token_of(n);
     const int bits = v_side ? a.v_bits : a.k_bits;
-    const uint32_t lane_word = L::TABLE | uint32_t(lane * 4) | (v_side ? 128u : 0u);
+    const uint32_t lane_word = L::TABLE | uint32_t((lane & (L::COPIES - 1)) * 4) | (v_side ? L::VTABLE : 0u);
     const uint32_t piece0 = L::piece(0, v_side, tok / L::PR);
     Cursor c(a, range);
     uint32_t kw[2][4];  // rows that no box moves (d = 64)
@@ -813,11 +832,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           for (int it = sub * L::TURNS; it < (sub + 1) * L::TURNS; ++it) {
             uint32_t w[4];
             read_octets<D, B>(piece, tok % L::PR, it, w);
-            put_octets<B>(w, dst + uint32_t(it >> 1) * (TN * 128), (it & 1) * 4, n, lane_word);
+            put_octets<L::COPIES, B>(w, dst + uint32_t(it >> 1) * (TN * 128), (it & 1) * 4, n, lane_word);
           }
         } else {
-          put_octets<B>(cw[0], dst, 0, n, lane_word);
-          put_octets<B>(cw[1], dst, 4, n, lane_word);
+          put_octets<L::COPIES, B>(cw[0], dst, 0, n, lane_word);
+          put_octets<L::COPIES, B>(cw[1], dst, 4, n, lane_word);
         }
       };
       switch (bits) {
@@ -892,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             const uint64_t k0 = smem_desc_sw128(L::K0 + uint32_t(j & 1) * 0x8000u);
             if (few) {
 #pragma unroll
-              for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                   tc_mma_f16(d, k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4),
@@ -900,11 +919,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                              L::idesc(16), uint32_t(part + ks > 0));
             } else {
 #pragma unroll
-              for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                  tc_mma_f16_ts(d, tm + uint32_t((part ? L::QL : L::Q) + 8 * ks),
-                                k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), L::idesc(TN), uint32_t(part + ks > 0));
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint64_t k = k0 + uint64_t(((ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4);
+                  if (D > 128 && part)
+                    tc_mma_f16(d, smem_desc_sw128(L::qlow(ks >> 2)) + uint64_t(((ks & 3) * 32) >> 4), k, L::idesc(TN), 1u);
+                  else
+                    tc_mma_f16_ts(d, tm + uint32_t((part ? L::QL : L::Q) + 8 * ks), k, L::idesc(TN), uint32_t(part + ks > 0));
+                }
             }
             mma_commit(s_full(j));
           }
