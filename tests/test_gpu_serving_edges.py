@@ -7,6 +7,8 @@ test_gpu_serving.py unless a test derives its own."""
 from __future__ import annotations
 
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -15,6 +17,7 @@ import torch
 from oracle import rrq as orc
 from oracle import serving as osv
 from random_rotation_kv_b200 import binding as B
+from tests.conftest import ROOT
 from tests.test_gpu_serving import DEV, HALF, _attend, _check_attention, _check_mass, _dev, _part
 
 pytestmark = pytest.mark.gpu
@@ -342,3 +345,39 @@ def test_evicted_caches_grow():
     host = [x.reshape(-1, *x.shape[3:]).cpu().numpy() for x in new]
     _check_attention(rg.standard_normal((batch, hq, d)), None, host, (at + 1).tolist(), hkv, d, 4, 4, d ** -0.5, torch.float16,
                      "grown")
+
+
+FIRST_CALLS_CAPTURED = """
+import torch
+from random_rotation_kv_b200 import binding as B
+dev = "cuda:0"
+gen = torch.Generator(device=dev).manual_seed(1)
+
+def part(*lead):
+    return [x for _ in range(2) for x in (torch.randint(0, 256, (*lead, 64), device=dev, generator=gen).to(torch.uint8),
+                                          torch.rand(*lead, device=dev, generator=gen) + 0.5)]
+
+q, pos = torch.randn(3, 8, 128, device=dev, generator=gen).half(), torch.arange(3, device=dev)
+p, t, lens = part(200, 2), part(3, 50, 2), torch.tensor([50, 0, 7], dtype=torch.int32, device=dev)
+scores, freqs = torch.randn(3, 8, 50, device=dev, generator=gen), B.rrq_rope_frequencies(128)[0]
+
+def step():
+    turned = B.rrq_rope(q, pos, freqs)
+    out = B.rrq_attention_shared(turned, *p, *t, lens, 2, 128, 1, 2, scale=0.1)
+    mass = B.rrq_attention_mass(scores, 2, lens=lens)
+    return [turned, out, mass, *B.rrq_evict(mass, lens, 20, *t, sink=1, recent=2)]
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(held, step()))
+print("captured")
+"""
+
+
+def test_serving_calls_captured_before_any_other():
+    """A process whose first use of the calls is a capture."""
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert done.returncode == 0 and "captured" in done.stdout, done.stderr[-2000:]
