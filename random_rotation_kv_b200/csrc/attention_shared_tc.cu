@@ -11,7 +11,7 @@
 // grows by more than 6 (powers of two), so O is rarely rescaled; P is at most 2^15.  In a full
 // tile whose value norms lie within 2^5 of one another max x + max log2 ν^V stands for the
 // maximum, at most 5 above it, without a second number per token (64 sequences on a prefix of
-// 32768 tokens: 134 us, with the sum taken for every token 141); so P keeps 11 bits down
+// 32768 tokens: 127 us, with the sum taken for every token 141); so P keeps 11 bits down
 // to 2^-18 of the row's largest at least.  Norms below 2^-90 count as 2^-90 in m, which keeps
 // 2^{x − m'} and its sum within fp32's range.  The state (m', Σ 2^{x − m'}, O) is what the
 // merge takes.
@@ -294,6 +294,33 @@ __device__ __forceinline__ void mask(float2 (&y)[16], int h, int valid, float v)
     if (token_of(n) >= valid) y[k].x = v;
     if (token_of(n + 1) >= valid) y[k].y = v;
   }
+}
+
+// The largest x + log2 ν over columns [from, from + TN/2) of a tile, token by token (`sb`: their tensor
+// memory, `nk`: their key norms).  Not inlined: next to the common way it cost registers there.
+template <int TN> __device__ __noinline__ float largest_sum(uint32_t sb, uint32_t nk, int from, int valid, float rs) {
+  const uint32_t lv = nk + (Tc<128>::LV - Tc<128>::NK);  // for every D
+  const float2 rs2 = make_float2(rs, rs);
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int h = 0; h < TN / 2; h += 32) {
+    uint32_t v[32];
+    tmem_ld32(sb + h, v);
+    tmem_ld_wait();
+    float2 y[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 n = lds_f4(nk + uint32_t(h + k) * 4), g = lds_f4(lv + uint32_t(h + k) * 4);
+      const float2 s0 = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+      const float2 s1 = make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+      y[k / 2] = fma2(mul2(s0, make_float2(n.x, n.y)), rs2, make_float2(g.x, g.y));
+      y[k / 2 + 1] = fma2(mul2(s1, make_float2(n.z, n.w)), rs2, make_float2(g.z, g.w));
+    }
+    mask(y, from + h, valid, -INFINITY);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) mx = fmaxf(mx, fmaxf(fmaxf(y[k].x, y[k].y), fmaxf(y[k + 1].x, y[k + 1].y)));
+  }
+  return mx;
 }
 
 // Position in a range's segments, one tile at a time.
@@ -608,15 +635,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             const int left = s.tokens - i * TN, valid = left < TN ? left : TN;
             const bool full = valid == TN;
             const uint32_t sb = tl + uint32_t(L::S + (j & 1) * TN + half * TH);
-            const uint32_t nk = L::NK + uint32_t((j & 3) * TN + half * TH) * 4, nv = nk + (L::NV - L::NK), lv = nk + (L::LV - L::NK);
+            const uint32_t nk = L::NK + uint32_t((j & 3) * TN + half * TH) * 4, nv = nk + (L::NV - L::NK);
             const uint32_t xch = L::XCH + uint32_t(j & 1) * 1024 + uint32_t(ln) * 4;
             const float2 rs2 = make_float2(rs, rs);
             float mx = -INFINITY;
             if (ok) {
-              // the largest x + log2 ν of the row's half (loops kept rolled: unrolled, the warps'
-              // different code ran out of the instruction cache)
+              // the largest x + log2 ν of the row's half, by way of the largest x where the norms allow it
+              // (loops kept rolled: unrolled, the warps' different code ran out of the instruction cache)
               const float2 range = log2_range<TN>(L::LRANGE, j);
-              auto largest = [&](auto tight) {
+              if (full) {
 #pragma unroll 1
                 for (int h = 0; h < TH; h += 32) {
                   uint32_t v[32];
@@ -630,23 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                     const float4 n = lds_f4(nk + uint32_t(h + k) * 4);
                     y[k / 2] = mul2(y[k / 2], make_float2(n.x, n.y));
                     y[k / 2 + 1] = mul2(y[k / 2 + 1], make_float2(n.z, n.w));
-                    if constexpr (!decltype(tight)::value) {
-                      const float4 g = lds_f4(lv + uint32_t(h + k) * 4);
-                      y[k / 2] = fma2(y[k / 2], rs2, make_float2(g.x, g.y));
-                      y[k / 2 + 1] = fma2(y[k / 2 + 1], rs2, make_float2(g.z, g.w));
-                    }
                   }
-                  if constexpr (!decltype(tight)::value) mask(y, half * TH + h, valid, -INFINITY);
 #pragma unroll
                   for (int k = 0; k < 16; k += 2) mx = fmaxf(mx, fmaxf(fmaxf(y[k].x, y[k].y), fmaxf(y[k + 1].x, y[k + 1].y)));
                 }
-              };
-              if (full && range.x - range.y <= kTight) {
-                largest(std::true_type{});
-                mx = fmaf(mx, rs, range.x);
-              } else {
-                largest(std::false_type{});
               }
+              if (full && range.x - range.y <= kTight) mx = fmaf(mx, rs, range.x);
+              else mx = largest_sum<TN>(sb, nk, half * TH, valid, rs);
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + uint32_t(half) * 512), "f"(mx) : "memory");
             }
             ok = meet(pair, 64, ok);
