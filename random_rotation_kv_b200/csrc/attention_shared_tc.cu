@@ -11,20 +11,23 @@
 // grows by more than 6 (powers of two), so O is rarely rescaled; P is at most 2^15.  In a full
 // tile whose value norms lie within 2^5 of one another max x + max log2 ν^V stands for the
 // maximum, at most 5 above it, without a second number per token (64 sequences on a prefix of
-// 32768 tokens: 127 us, with the sum taken for every token 141); so P keeps 11 bits down
-// to 2^-18 of the row's largest at least.  Norms below 2^-90 count as 2^-90 in m, which keeps
-// 2^{x − m'} and its sum within fp32's range.  The state (m', Σ 2^{x − m'}, O) is what the
-// merge takes.
+// 32768 tokens: 125 us; 152 where the norms spread by e in either direction, so that no tile
+// is of that kind); so P keeps 11 bits down
+// to 2^-18 of the row's largest at least.  It is one fp16 part: 2^-12 of a weight on average,
+// no more than fp16 outputs are rounded by, while a second would take another product.  Norms
+// below 2^-90 count as 2^-90 in m, which keeps 2^{x − m'} and its sum within fp32's range.  The
+// state (m', Σ 2^{x − m'}, O) is what the merge takes.
 //
 // Units of at most 16 rows (d ≤ 128) exchange the operands' roles: a tile's 128 tokens are the
 // rows of Sᵀ = C_K·Q'ᵀ and the coordinates the rows of Oᵀ = C_Vᵀ·Pᵀ, 16 columns wide, so that a
 // thread has a token's 8 rows to weigh instead of a row's 64 tokens of which most
-// rows would be empty (33 sequences x 4 heads of up to 1500 tokens, 4 rows a unit: 23 us against 27
-// without; 64 x 8 tails behind a prefix of 32768 tokens: 127 against 159).
+// rows would be empty (33 sequences x 4 heads of up to 1500 tokens, 4 rows a unit: 22 us against 33
+// without; 64 x 8 tails behind a prefix of 32768 tokens: 128 against 168).
 //
 // Bound by the latency of the weight warps' two passes (about 3600 of a tile's 4400 cycles at 128
 // rows): 64 sequences x 32 heads on 32768 + 1024 tokens x 8 heads take 125 us, 280 TFLOP/s,
-// against 21 us of products at the tensor cores' rate; 16 sequences on 4096 tokens 27 us.
+// against 21 us of products at the tensor cores' rate (32 with the queries' second part); 16
+// sequences on 4096 tokens 28 us.
 //
 // One CTA per SM walks its range of tiles (128 tokens, 64 for d = 256), 19 warps:
 //  * warp 17 copies the packed codes of two tiles ahead into shared memory (TMA boxes of
@@ -32,7 +35,7 @@
 //    are not multiples of TMA's 16 and are read by the filling warps themselves);
 //  * warps 8–11 and 12–15 turn K and V codes into fp16 levels, one token per thread, by one
 //    shared-memory lookup per byte of two coordinates (tables of 256 pairs, one copy per lane
-//    so that no bank conflicts), and write rows [token][coordinate] in the 128-byte swizzle,
+//    so that no bank conflicts; at d = 256 eight copies), and write rows [token][coordinate] in the 128-byte swizzle,
 //    K in two stages: as they lie, K is a K-major operand and V, whose tokens are summed over,
 //    an MN-major one.  Row 8k + e of a tile's 64 is token 8k + (e + k) mod 8, so the eight
 //    lanes that share a wavefront read eight neighbouring code rows;
@@ -43,7 +46,7 @@
 // Tensor memory: S twice, O and the queries, of which d = 256 has room for the first part only (512
 // columns in use): its second part is an operand in shared memory, in place of three quarters of
 // the tables' copies and of what few rows take elsewhere (32 sequences x 32/8 heads on 8192
-// tokens 66 us, with one part of 11 bits and all copies 52; 7 x 16/4 heads on 2049: 25.4 and 22.4).
+// tokens 65 us, with one part of 11 bits and all copies 52; 7 x 16/4 heads on 2049: 25 and 22).
 // Every wait is bounded; a wait that gives up makes the CTA's states NaN.
 #include <cstring>
 
@@ -61,8 +64,8 @@ constexpr int kFill = 128;  // threads that fill K, and as many that fill V
 constexpr float kGrowth = 6.f, kRoom = 9.f;  // of a row's maximum before m' moves; of the weights above it
 constexpr float kTight = 5.f;  // powers of two that a tile's value norms may span for the short way to m
 // Rows of a unit that exchanges the operands' roles, as many as its 16 columns hold: 33 x 4 tails of up
-// to 1500 tokens at 4, 8, 12 and 16 rows 22, 24, 26 and 26 us (29, 29, 33 and 34 without); one
-// sequence of 65536 tokens x 8 heads 54, 55, 58 and 58 (62, 63, 64 and 64).
+// to 1500 tokens at 4, 8, 12 and 16 rows 22, 23, 24 and 24 us (30, 32, 36 and 36 without); one
+// sequence of 65536 tokens x 8 heads 53, 54, 57 and 57 (63, 65, 65 and 66).
 constexpr int kFewRows = 16;
 constexpr int kThreads = (kSoftWarps + kFillWarps + 3) * 32;
 
@@ -297,8 +300,9 @@ __device__ __forceinline__ void mask(float2 (&y)[16], int h, int valid, float v)
 }
 
 // The largest x + log2 ν over columns [from, from + TN/2) of a tile, token by token (`sb`: their tensor
-// memory, `nk`: their key norms).  Not inlined: next to the common way it cost registers there.
-template <int TN> __device__ __noinline__ float largest_sum(uint32_t sb, uint32_t nk, int from, int valid, float rs) {
+// memory, `nk`: their key norms).  Not inlined: next to the common way it cost registers there, 133 us
+// instead of 125 for 64 sequences on a prefix of 32768 tokens.
+template <int TN, bool WHOLE> __device__ __noinline__ float largest_sum(uint32_t sb, uint32_t nk, int from, int valid, float rs) {
   const uint32_t lv = nk + (Tc<128>::LV - Tc<128>::NK);  // for every D
   const float2 rs2 = make_float2(rs, rs);
   float mx = -INFINITY;
@@ -316,7 +320,7 @@ template <int TN> __device__ __noinline__ float largest_sum(uint32_t sb, uint32_
       y[k / 2] = fma2(mul2(s0, make_float2(n.x, n.y)), rs2, make_float2(g.x, g.y));
       y[k / 2 + 1] = fma2(mul2(s1, make_float2(n.z, n.w)), rs2, make_float2(g.z, g.w));
     }
-    mask(y, from + h, valid, -INFINITY);
+    if constexpr (!WHOLE) mask(y, from + h, valid, -INFINITY);
 #pragma unroll
     for (int k = 0; k < 16; k += 2) mx = fmaxf(mx, fmaxf(fmaxf(y[k].x, y[k].y), fmaxf(y[k + 1].x, y[k + 1].y)));
   }
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               // the largest x + log2 ν of the row's half, by way of the largest x where the norms allow it
               // (loops kept rolled: unrolled, the warps' different code ran out of the instruction cache)
               const float2 range = log2_range<TN>(L::LRANGE, j);
-              if (full) {
+              if (full && range.x - range.y <= kTight) {
 #pragma unroll 1
                 for (int h = 0; h < TH; h += 32) {
                   uint32_t v[32];
@@ -661,9 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 #pragma unroll
                   for (int k = 0; k < 16; k += 2) mx = fmaxf(mx, fmaxf(fmaxf(y[k].x, y[k].y), fmaxf(y[k + 1].x, y[k + 1].y)));
                 }
+                mx = fmaf(mx, rs, range.x);
+              } else {
+                mx = full ? largest_sum<TN, true>(sb, nk, half * TH, valid, rs) : largest_sum<TN, false>(sb, nk, half * TH, valid, rs);
               }
-              if (full && range.x - range.y <= kTight) mx = fmaf(mx, rs, range.x);
-              else mx = largest_sum<TN>(sb, nk, half * TH, valid, rs);
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + uint32_t(half) * 512), "f"(mx) : "memory");
             }
             ok = meet(pair, 64, ok);
