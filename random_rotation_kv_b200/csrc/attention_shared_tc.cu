@@ -11,12 +11,11 @@
 // grows by more than 6 (powers of two), so O is rarely rescaled; P is at most 2^15.  In a full
 // tile whose value norms lie within 2^5 of one another max x + max log2 ν^V stands for the
 // maximum, at most 5 above it, without a second number per token (64 sequences on a prefix of
-// 32768 tokens: 125 us; 152 where the norms spread by e in either direction, so that no tile
-// is of that kind); so P keeps 11 bits down
-// to 2^-18 of the row's largest at least.  It is one fp16 part: 2^-12 of a weight on average,
-// no more than fp16 outputs are rounded by, while a second would take another product.  Norms
-// below 2^-90 count as 2^-90 in m, which keeps 2^{x − m'} and its sum within fp32's range.  The
-// state (m', Σ 2^{x − m'}, O) is what the merge takes.
+// 32768 tokens: 125 us; 152 where the norms' logarithms deviate by 1, so that no tile is of
+// that kind); so P keeps 11 bits down to 2^-18 of the row's largest at least.  It is one fp16
+// part: 2^-12 of a weight on average, no more than fp16 outputs are rounded by, while a second
+// would take another product.  Norms below 2^-90 count as 2^-90 in m, which keeps 2^{x − m'}
+// and its sum within fp32's range.  The state (m', Σ 2^{x − m'}, O) is what the merge takes.
 //
 // Units of at most 16 rows (d ≤ 128) exchange the operands' roles: a tile's 128 tokens are the
 // rows of Sᵀ = C_K·Q'ᵀ and the coordinates the rows of Oᵀ = C_Vᵀ·Pᵀ, 16 columns wide, so that a

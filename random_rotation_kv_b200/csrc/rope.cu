@@ -13,8 +13,8 @@
 // cosine serve every head the thread walks; the heads are spread over more threads only
 // while there are too few tokens to fill the GPU.  Pairs that do not come in eights
 // (rot not a multiple of 16) and addresses off 32 bytes take one pair per thread.
-// 32768 x 8 x 128 fp16: 22-24 us, 5.6-6.0 TB/s (one pair per thread: 46 us); one token of 32
-// heads: 1.8 us.
+// 32768 x 8 x 128 fp16: 22-24 us, 5.6-6.0 TB/s; with 90 or 40 of the 128 coordinates turned (one pair
+// per thread, bound by the number of its 2-byte accesses) 70 and 65 us; one token of 32 heads: 1.8 us.
 #include <cstring>
 
 #include "rope.h"
