@@ -353,9 +353,9 @@ size_t rrq_attention_workspace_bytes(int hq, int hkv, int d, int k_bits, int v_b
  *    3.8e-5 on average;
  *  - the rotated queries: 22 bits.
  * A score is therefore off by at most 2^-11·scale·‖q‖·‖k̂_t‖, and √d times less on average, all
- * but 2^-11 of it from the key levels.  While that stays below 5e-4, and no more than 2^18 tokens of a head have weights below 2^-18 of its largest,
- * the output of a head is within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is rounded to
- * q_dtype.
+ * but 2^-11 of it from the key levels.  While the scores' errors stay below 5e-4, and no more
+ * than 2^18 tokens of a head have weights below 2^-18 of its largest, the output of a head is
+ * within 2e-3·Σ_t p_t·‖v̂_t‖ of the exact one before it is rounded to q_dtype.
  * Errors: RRQ_ERR_INVALID (incl. a workspace that is too small), RRQ_ERR_UNSUPPORTED
  * (q_dtype RRQ_F32, more than 128 heads per kv head, 2^31 − 128 or more tokens in the
  * prefix or over all tails, 10^8 or more tiles of 64 or 128 tokens over all units of work,

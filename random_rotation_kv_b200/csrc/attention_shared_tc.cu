@@ -100,7 +100,8 @@ template <int D> struct Tc {
   static constexpr int S = 0, O = 2 * TN, Q = O + D, QL = Q + D / 2;
   // fp16 operands, fp32 sums, M = 128; bits 15 and 16: A, B MN-major
   static constexpr uint32_t idesc(int n) { return (1u << 4) | (uint32_t(n / 8) << 17) | ((128u / 16) << 24); }
-  static_assert(LV + 4 * TN * 4 <= PT && TABLE + 256 * 2 * COPIES * 4 <= (D <= 128 ? K0 : qlow(0)) && qlow(3) + 0x4000 <= XCH && TILE <= 0x8000 && kTotal <= 227 * 1024, "layout");
+  static_assert(LV + 4 * TN * 4 <= PT && TABLE + 256 * 2 * COPIES * 4 <= (D <= 128 ? K0 : 0x14000u) && TILE <= 0x8000 &&
+                    kTotal <= 227 * 1024, "layout");
 };
 
 // Token of row (column of S) n of a tile.
